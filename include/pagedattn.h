@@ -448,7 +448,8 @@ pa_status attn_tree_paged_fp8(const pa_plan_params* params, const void* d_ws, si
  * rows target_pitch, draft_pitch >= vocab values apart (draft_pitch 0 without draft rows);
  * vocab <= 2^20.  d_u_accept fp32 [sum n] (node 0's is not read), d_u_final fp32 [B].
  * d_accept_len int32 [B]: drafted nodes accepted;  d_accept_path int32 [B][path_pitch]: 0, then
- * the accepted nodes in order, then -1; at most path_pitch - 1 nodes are accepted;
+ * the accepted nodes in order, then -1 (path_pitch values a row are written); at most path_pitch - 1
+ * nodes are accepted;
  * d_next_token int32 [B].  A request without nodes, or whose node 0 is not in use, gives 0, -1s, -1.
  * d_ws            optional plan workspace: bad rows, parents and tokens (their child is not
  *                 asked) are recorded in its error word.

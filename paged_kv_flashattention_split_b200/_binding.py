@@ -289,7 +289,7 @@ def attn_tree_verify(cu_seqlens_q, parent, tokens, target_probs, draft_probs, u_
                      accept_path, next_token, ws=None, max_q_tokens=None, vocab=None, stream=None,
                      raise_on_error=True) -> int:
     """Verify drafted tokens against the target's rows ([sum n, vocab] fp32, rows any stride >= vocab apart;
-    draft_probs the same, or None); writes accept_len [B], accept_path [B, pitch], next_token [B] (int32)."""
+    draft_probs the same, or None); writes accept_len [B], accept_path [B, width] (dense), next_token [B] (int32)."""
     batch = accept_len.shape[0]
     rows = parent.shape[0] if max_q_tokens is None else max_q_tokens
     vocab = target_probs.shape[-1] if vocab is None else vocab
@@ -298,7 +298,7 @@ def attn_tree_verify(cu_seqlens_q, parent, tokens, target_probs, draft_probs, u_
     st = lib().attn_tree_verify(int(batch), int(rows), int(vocab), _ptr(cu_seqlens_q), _ptr(parent), _ptr(tokens),
                                 _ptr(target_probs), _row_pitch(target_probs), _ptr(draft_probs),
                                 0 if draft_probs is None else _row_pitch(draft_probs), _ptr(u_accept), _ptr(u_final),
-                                _ptr(accept_len), _ptr(accept_path), _row_pitch(accept_path), _ptr(next_token),
+                                _ptr(accept_len), _ptr(accept_path), _path_width(accept_path, batch), _ptr(next_token),
                                 _ptr(ws), _stream(stream))
     return _check(st, "attn_tree_verify", raise_on_error)
 
@@ -308,6 +308,14 @@ def _row_pitch(t) -> int:
     if t.dim() != 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError("a matrix with dense rows is needed")
     return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[-1]))
+
+
+def _path_width(path, batch) -> int:
+    """Width of the accepted paths.  The kernels take it for the rows' stride too and fill rows to it, so the rows
+    are dense: columns inside longer rows are refused."""
+    if path.dim() != 2 or path.shape[0] < batch or not path.is_contiguous():
+        raise ValueError("the accepted paths need a dense matrix with a row for each request")
+    return int(path.shape[1])
 
 
 class PoolList:
@@ -334,14 +342,15 @@ def make_pool_list(pools) -> PoolList:
 def attn_kv_compact(pool_list, seq_lens, cu_seqlens_q, accept_len, accept_path, page_table, page_size,
                     seq_lens_out=None, ws=None, max_q_tokens=None, pt_pitch=None, stream=None,
                     raise_on_error=True) -> int:
-    """Move the accepted nodes' rows behind the prefixes, in every pool of pool_list (make_pool_list)."""
+    """Move the accepted nodes' rows behind the prefixes, in every pool of pool_list (make_pool_list);
+    accept_path as attn_tree_verify writes it ([B, width], dense)."""
     batch = accept_len.shape[0]
     # without a bound on the rows: what the batch can hold
     rows = 256 * batch if max_q_tokens is None else max_q_tokens
     pt_pitch = page_table.shape[-1] if pt_pitch is None else pt_pitch
     st = lib().attn_kv_compact(pool_list.array, len(pool_list.pools), pool_list.hkv, pool_list.head_dim,
                                pool_list.elem_bytes, pool_list.num_slots, int(batch), int(rows), _ptr(seq_lens),
-                               _ptr(cu_seqlens_q), _ptr(accept_len), _ptr(accept_path), _row_pitch(accept_path),
+                               _ptr(cu_seqlens_q), _ptr(accept_len), _ptr(accept_path), _path_width(accept_path, batch),
                                _ptr(page_table), int(pt_pitch), int(page_size), _ptr(seq_lens_out), _ptr(ws),
                                _stream(stream))
     return _check(st, "attn_kv_compact", raise_on_error)

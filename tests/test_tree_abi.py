@@ -196,3 +196,56 @@ def test_compaction_oracle():
                                  np.array([[2, 0, 1], [3, 4, 5]]), 2)
     # request 0: prefix 2 at slots 4 5, nodes at 0 1 2 3; node 2 -> position 3 (slot 1), node 3 -> position 4 (slot 2)
     assert new[:, 0].tolist() == [0, 2, 3, 3, 4, 5, 6, 7, 8, 9, 10, 11] and lens.tolist() == [5, 1]
+
+
+# ------------------------------------------------------------------------------------- arguments of the binding
+
+def step_arguments(B=2, T=6, vocab=40, pitch=4):
+    """Arguments of a verification and of a compaction over host memory: they are to be refused before any launch."""
+    i32 = dict(dtype=torch.int32)
+    verify = dict(cu_seqlens_q=torch.zeros(B + 1, **i32), parent=torch.zeros(T, **i32), tokens=torch.zeros(T, **i32),
+                  target_probs=torch.zeros(T, vocab), draft_probs=torch.zeros(T, vocab), u_accept=torch.zeros(T),
+                  u_final=torch.zeros(B), accept_len=torch.zeros(B, **i32), accept_path=torch.zeros(B, pitch, **i32),
+                  next_token=torch.zeros(B, **i32))
+    compact = dict(pool_list=pa.make_pool_list([torch.zeros(16, 2, 128, dtype=torch.bfloat16)]),
+                   seq_lens=torch.zeros(B, **i32), cu_seqlens_q=torch.zeros(B + 1, **i32),
+                   accept_len=torch.zeros(B, **i32), accept_path=torch.zeros(B, pitch, **i32),
+                   page_table=torch.zeros(B, 4, **i32), page_size=4, seq_lens_out=torch.zeros(B, **i32))
+    return verify, compact
+
+
+@pytest.mark.parametrize("path", [
+    lambda: torch.zeros(2, 10, dtype=torch.int32)[:, 2:8],         # columns inside longer rows
+    lambda: torch.zeros(2, 10, dtype=torch.int32)[:, :4],
+    lambda: torch.zeros(4, 2, dtype=torch.int32).t(),
+    lambda: torch.zeros(8, dtype=torch.int32),                     # no rows
+    lambda: torch.zeros(1, 4, dtype=torch.int32),                  # fewer rows than requests
+])
+def test_accepted_paths_are_dense_rows(lib, path):
+    """The kernels take the width of a path for its stride: a fill of wider rows would leave the view."""
+    verify, compact = step_arguments()
+    with pytest.raises(ValueError, match="path"):
+        pa.attn_tree_verify(**dict(verify, accept_path=path()))
+    with pytest.raises(ValueError, match="path"):
+        pa.attn_kv_compact(**dict(compact, accept_path=path()))
+
+
+def test_one_accepted_path_out_of_longer_rows_has_its_own_width(lib, monkeypatch):
+    """A single row is dense whatever its stride; its pitch is its width."""
+    verify, compact = step_arguments(B=1, T=3)
+    view = torch.zeros(1, 10, dtype=torch.int32)[:, 2:8]
+    seen = {}
+
+    class Fake:
+        def attn_tree_verify(self, *args):
+            seen["verify"] = args[14]
+            return pa.PA_OK
+
+        def attn_kv_compact(self, *args):
+            seen["compact"] = args[12]
+            return pa.PA_OK
+
+    monkeypatch.setattr(pa._binding, "lib", lambda: Fake())
+    pa.attn_tree_verify(**dict(verify, accept_path=view))
+    pa.attn_kv_compact(**dict(compact, accept_path=view))
+    assert seen == dict(verify=6, compact=6)
