@@ -295,26 +295,40 @@ def attn_tree_verify(cu_seqlens_q, parent, tokens, target_probs, draft_probs, u_
     vocab = target_probs.shape[-1] if vocab is None else vocab
     if min(t.shape[-1] for t in (target_probs, draft_probs) if t is not None) < vocab:
         raise ValueError("rows of probabilities shorter than the vocabulary")
-    st = lib().attn_tree_verify(int(batch), int(rows), int(vocab), _ptr(cu_seqlens_q), _ptr(parent), _ptr(tokens),
-                                _ptr(target_probs), _row_pitch(target_probs), _ptr(draft_probs),
-                                0 if draft_probs is None else _row_pitch(draft_probs), _ptr(u_accept), _ptr(u_final),
-                                _ptr(accept_len), _ptr(accept_path), _path_width(accept_path, batch), _ptr(next_token),
+    i32, f32 = torch.int32, torch.float32
+    st = lib().attn_tree_verify(int(batch), int(rows), int(vocab), _vector("cu_seqlens_q", cu_seqlens_q, i32, batch + 1),
+                                _vector("parent", parent, i32), _vector("tokens", tokens, i32), _ptr(target_probs),
+                                _row_pitch("target_probs", target_probs), _ptr(draft_probs),
+                                0 if draft_probs is None else _row_pitch("draft_probs", draft_probs),
+                                _vector("u_accept", u_accept, f32), _vector("u_final", u_final, f32, batch),
+                                _vector("accept_len", accept_len, i32), _ptr(accept_path),
+                                _path_width(accept_path, batch), _vector("next_token", next_token, i32, batch),
                                 _ptr(ws), _stream(stream))
     return _check(st, "attn_tree_verify", raise_on_error)
 
 
-def _row_pitch(t) -> int:
-    """Elements between the rows of a matrix whose rows are dense."""
-    if t.dim() != 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError("a matrix with dense rows is needed")
+def _vector(name, t, dtype, n=0):
+    """Address of a dense tensor of at least n values of one type; an int is an address, None is NULL.  The kernels
+    read 32-bit words: 64-bit tokens, as argmax and topk give them, would be taken for other tokens."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: a dense {dtype} tensor of at least {n} values is needed")
+    return t.data_ptr()
+
+
+def _row_pitch(name, t) -> int:
+    """Elements between the rows of an fp32 matrix whose rows are dense."""
+    if t.dtype is not torch.float32 or t.dim() != 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: a float32 matrix with dense rows is needed")
     return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[-1]))
 
 
 def _path_width(path, batch) -> int:
     """Width of the accepted paths.  The kernels take it for the rows' stride too and fill rows to it, so the rows
     are dense: columns inside longer rows are refused."""
-    if path.dim() != 2 or path.shape[0] < batch or not path.is_contiguous():
-        raise ValueError("the accepted paths need a dense matrix with a row for each request")
+    if path.dtype is not torch.int32 or path.dim() != 2 or path.shape[0] < batch or not path.is_contiguous():
+        raise ValueError("accept_path: a dense torch.int32 matrix with a row for each request is needed")
     return int(path.shape[1])
 
 
@@ -347,12 +361,19 @@ def attn_kv_compact(pool_list, seq_lens, cu_seqlens_q, accept_len, accept_path, 
     batch = accept_len.shape[0]
     # without a bound on the rows: what the batch can hold
     rows = 256 * batch if max_q_tokens is None else max_q_tokens
-    pt_pitch = page_table.shape[-1] if pt_pitch is None else pt_pitch
+    i32 = torch.int32
+    if pt_pitch is None:
+        pt_pitch = page_table.shape[-1]
+        table = _vector("page_table", page_table, i32, batch * pt_pitch)
+    else:
+        table = _ptr(page_table)
     st = lib().attn_kv_compact(pool_list.array, len(pool_list.pools), pool_list.hkv, pool_list.head_dim,
-                               pool_list.elem_bytes, pool_list.num_slots, int(batch), int(rows), _ptr(seq_lens),
-                               _ptr(cu_seqlens_q), _ptr(accept_len), _ptr(accept_path), _path_width(accept_path, batch),
-                               _ptr(page_table), int(pt_pitch), int(page_size), _ptr(seq_lens_out), _ptr(ws),
-                               _stream(stream))
+                               pool_list.elem_bytes, pool_list.num_slots, int(batch), int(rows),
+                               _vector("seq_lens", seq_lens, i32, batch),
+                               _vector("cu_seqlens_q", cu_seqlens_q, i32, batch + 1),
+                               _vector("accept_len", accept_len, i32), _ptr(accept_path),
+                               _path_width(accept_path, batch), table, int(pt_pitch), int(page_size),
+                               _vector("seq_lens_out", seq_lens_out, i32, batch), _ptr(ws), _stream(stream))
     return _check(st, "attn_kv_compact", raise_on_error)
 
 

@@ -249,3 +249,64 @@ def test_one_accepted_path_out_of_longer_rows_has_its_own_width(lib, monkeypatch
     pa.attn_tree_verify(**dict(verify, accept_path=view))
     pa.attn_kv_compact(**dict(compact, accept_path=view))
     assert seen == dict(verify=6, compact=6)
+
+
+@pytest.mark.parametrize("name,wrong", [
+    (name, wrong) for name in ("cu_seqlens_q", "parent", "tokens", "accept_len", "accept_path", "next_token")
+    for wrong in (torch.int64, torch.float32)] + [
+    (name, wrong) for name in ("target_probs", "draft_probs", "u_accept", "u_final")
+    for wrong in (torch.bfloat16, torch.float64, torch.int32)])
+def test_verification_refuses_other_types(lib, name, wrong):
+    """The kernel reads 32-bit words: 64-bit tokens (as argmax and topk give) would be taken for other tokens."""
+    verify, _ = step_arguments()
+    with pytest.raises(ValueError, match=name):
+        pa.attn_tree_verify(**dict(verify, **{name: verify[name].to(wrong)}))
+
+
+@pytest.mark.parametrize("name", ["cu_seqlens_q", "parent", "tokens", "u_accept", "u_final", "accept_len", "next_token"])
+def test_verification_refuses_strided_vectors(lib, name):
+    verify, _ = step_arguments()
+    strided = torch.zeros(len(verify[name]), 2, dtype=verify[name].dtype)[:, 0]
+    with pytest.raises(ValueError, match=name):
+        pa.attn_tree_verify(**dict(verify, **{name: strided}))
+
+
+@pytest.mark.parametrize("name", ["cu_seqlens_q", "u_final", "next_token"])
+def test_verification_refuses_vectors_shorter_than_the_batch(lib, name):
+    verify, _ = step_arguments()
+    with pytest.raises(ValueError, match=name):
+        pa.attn_tree_verify(**dict(verify, **{name: verify[name][:-1]}))
+
+
+@pytest.mark.parametrize("name", ["seq_lens", "cu_seqlens_q", "accept_len", "accept_path", "page_table", "seq_lens_out"])
+def test_compaction_refuses_other_types_and_strides(lib, name):
+    _, compact = step_arguments()
+    t = compact[name]
+    wrong = [t.to(torch.int64), t.to(torch.float32), torch.stack([t, t], -1)[..., 0]]
+    for bad in wrong:
+        with pytest.raises(ValueError, match="path" if name == "accept_path" else name):
+            pa.attn_kv_compact(**dict(compact, **{name: bad}))
+    if name in ("seq_lens", "cu_seqlens_q", "page_table", "seq_lens_out"):
+        with pytest.raises(ValueError, match=name):
+            pa.attn_kv_compact(**dict(compact, **{name: t[:-1]}))
+
+
+def test_addresses_are_taken_as_they_are(lib, monkeypatch):
+    """A device address instead of a tensor has no type to check."""
+    verify, compact = step_arguments()
+    seen = []
+
+    class Fake:
+        def attn_tree_verify(self, *args):
+            seen.append(args)
+            return pa.PA_OK
+
+        def attn_kv_compact(self, *args):
+            seen.append(args)
+            return pa.PA_OK
+
+    monkeypatch.setattr(pa._binding, "lib", lambda: Fake())
+    pa.attn_tree_verify(**dict(verify, tokens=4096, u_accept=8192, draft_probs=None))
+    pa.attn_kv_compact(**dict(compact, seq_lens=4096, seq_lens_out=None))
+    assert seen[0][5] == 4096 and seen[0][10] == 8192 and seen[0][8] is None and seen[0][9] == 0
+    assert seen[1][8] == 4096 and seen[1][16] is None
