@@ -255,10 +255,45 @@ def attn_kv_store_sage(k8_new, v8_new, sf_k_new, out_cache_loc, k8_pool, v8_pool
     return _check(st, "attn_kv_store_sage", raise_on_error)
 
 
+def _vector(name, t, dtype, n=0):
+    """Address of a dense tensor of at least n values of one type; an int is an address, None is NULL.  The kernels
+    read 32-bit words: 64-bit tokens, as argmax and topk give them, would be taken for other tokens."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: a dense {dtype} tensor of at least {n} values is needed")
+    return t.data_ptr()
+
+
+_BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))          # bf16, or its bit patterns
+_BITS8 = frozenset((torch.uint8, torch.int8, torch.float8_e4m3fn))        # E4M3 codes
+
+
+def _dense(name, t, kinds):
+    """Address of a dense tensor of one of the given types (an int is an address, None is NULL)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in kinds or not t.is_contiguous():
+        raise ValueError(f"{name}: a dense tensor of one of {sorted(map(str, kinds))} is needed")
+    return t.data_ptr()
+
+
+def _table(page_table, batch, pt_pitch):
+    """Address and pitch of a page table: dense, or columns of longer rows with their pitch given."""
+    if pt_pitch is None:
+        pt_pitch = page_table.shape[-1]
+        return _vector("page_table", page_table, torch.int32, batch * pt_pitch), int(pt_pitch)
+    if isinstance(page_table, torch.Tensor) and page_table.dtype is not torch.int32:
+        raise ValueError("page_table: int32 is needed")
+    return _ptr(page_table), int(pt_pitch)
+
+
 def attn_plan_tree(params, seq_lens, cu_seqlens_q, parent, ws, stream=None, raise_on_error=True) -> int:
     """Plan of the draft-tree attention; parent int32 [sum n] (-1 a root, -2 a node not in use)."""
-    st = lib().attn_plan_tree(ctypes.byref(params), _ptr(seq_lens), _ptr(cu_seqlens_q), _ptr(parent), _ptr(ws),
-                              ws.numel() * ws.element_size(), _stream(stream))
+    batch, i32 = params.batch, torch.int32
+    st = lib().attn_plan_tree(ctypes.byref(params), _vector("seq_lens", seq_lens, i32, batch),
+                              _vector("cu_seqlens_q", cu_seqlens_q, i32, batch + 1), _vector("parent", parent, i32),
+                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     return _check(st, "attn_plan_tree", raise_on_error)
 
 
@@ -266,10 +301,11 @@ def attn_tree_paged(params, ws, q, k_pool, v_pool, page_table, sm_scale, out, ls
                     pt_pitch=None, stream=None, raise_on_error=True) -> int:
     """Draft-tree attention for one layer over a TREE plan; q and out bf16 [sum n, Hq, D]."""
     num_slots = k_pool.shape[0] if num_slots is None else num_slots
-    pt_pitch = page_table.shape[-1] if pt_pitch is None else pt_pitch
-    st = lib().attn_tree_paged(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _ptr(q), _ptr(k_pool),
-                               _ptr(v_pool), int(num_slots), _ptr(page_table), int(pt_pitch), float(sm_scale),
-                               _ptr(out), _ptr(lse_out), _stream(stream))
+    table, pt_pitch = _table(page_table, params.batch, pt_pitch)
+    st = lib().attn_tree_paged(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _dense("q", q, _BITS16),
+                               _dense("k_pool", k_pool, _BITS16), _dense("v_pool", v_pool, _BITS16), int(num_slots),
+                               table, pt_pitch, float(sm_scale), _dense("out", out, _BITS16),
+                               _vector("lse_out", lse_out, torch.float32), _stream(stream))
     return _check(st, "attn_tree_paged", raise_on_error)
 
 
@@ -277,10 +313,11 @@ def attn_tree_paged_fp8(params, ws, q, k8_pool, v8_pool, k_scale, v_scale, page_
                         num_slots=None, pt_pitch=None, stream=None, raise_on_error=True) -> int:
     """Draft-tree attention over E4M3 pools (uint8 codes) dequantised by k_scale / v_scale; q and out bf16."""
     num_slots = k8_pool.shape[0] if num_slots is None else num_slots
-    pt_pitch = page_table.shape[-1] if pt_pitch is None else pt_pitch
-    st = lib().attn_tree_paged_fp8(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _ptr(q),
-                                   _ptr(k8_pool), _ptr(v8_pool), float(k_scale), float(v_scale), int(num_slots),
-                                   _ptr(page_table), int(pt_pitch), float(sm_scale), _ptr(out), _ptr(lse_out),
+    table, pt_pitch = _table(page_table, params.batch, pt_pitch)
+    st = lib().attn_tree_paged_fp8(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _dense("q", q, _BITS16),
+                                   _dense("k8_pool", k8_pool, _BITS8), _dense("v8_pool", v8_pool, _BITS8),
+                                   float(k_scale), float(v_scale), int(num_slots), table, pt_pitch, float(sm_scale),
+                                   _dense("out", out, _BITS16), _vector("lse_out", lse_out, torch.float32),
                                    _stream(stream))
     return _check(st, "attn_tree_paged_fp8", raise_on_error)
 
@@ -305,16 +342,6 @@ def attn_tree_verify(cu_seqlens_q, parent, tokens, target_probs, draft_probs, u_
                                 _path_width(accept_path, batch), _vector("next_token", next_token, i32, batch),
                                 _ptr(ws), _stream(stream))
     return _check(st, "attn_tree_verify", raise_on_error)
-
-
-def _vector(name, t, dtype, n=0):
-    """Address of a dense tensor of at least n values of one type; an int is an address, None is NULL.  The kernels
-    read 32-bit words: 64-bit tokens, as argmax and topk give them, would be taken for other tokens."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: a dense {dtype} tensor of at least {n} values is needed")
-    return t.data_ptr()
 
 
 def _row_pitch(name, t) -> int:
@@ -362,17 +389,13 @@ def attn_kv_compact(pool_list, seq_lens, cu_seqlens_q, accept_len, accept_path, 
     # without a bound on the rows: what the batch can hold
     rows = 256 * batch if max_q_tokens is None else max_q_tokens
     i32 = torch.int32
-    if pt_pitch is None:
-        pt_pitch = page_table.shape[-1]
-        table = _vector("page_table", page_table, i32, batch * pt_pitch)
-    else:
-        table = _ptr(page_table)
+    table, pt_pitch = _table(page_table, batch, pt_pitch)
     st = lib().attn_kv_compact(pool_list.array, len(pool_list.pools), pool_list.hkv, pool_list.head_dim,
                                pool_list.elem_bytes, pool_list.num_slots, int(batch), int(rows),
                                _vector("seq_lens", seq_lens, i32, batch),
                                _vector("cu_seqlens_q", cu_seqlens_q, i32, batch + 1),
                                _vector("accept_len", accept_len, i32), _ptr(accept_path),
-                               _path_width(accept_path, batch), table, int(pt_pitch), int(page_size),
+                               _path_width(accept_path, batch), table, pt_pitch, int(page_size),
                                _vector("seq_lens_out", seq_lens_out, i32, batch), _ptr(ws), _stream(stream))
     return _check(st, "attn_kv_compact", raise_on_error)
 

@@ -310,3 +310,76 @@ def test_addresses_are_taken_as_they_are(lib, monkeypatch):
     pa.attn_kv_compact(**dict(compact, seq_lens=4096, seq_lens_out=None))
     assert seen[0][5] == 4096 and seen[0][10] == 8192 and seen[0][8] is None and seen[0][9] == 0
     assert seen[1][8] == 4096 and seen[1][16] is None
+
+
+def attention_arguments(fp8=False, B=2, T=6):
+    """Arguments of a tree plan and of one layer's attention over host memory."""
+    i32 = dict(dtype=torch.int32)
+    params = P(batch=B, max_q_tokens=T, max_kv_len=30)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    plan = dict(params=params, seq_lens=torch.zeros(B, **i32), cu_seqlens_q=torch.zeros(B + 1, **i32),
+                parent=torch.zeros(T, **i32), ws=ws)
+    kind = torch.uint8 if fp8 else torch.bfloat16
+    pools = [torch.zeros(64, 2, 128, dtype=kind) for _ in range(2)]
+    layer = dict(params=params, ws=ws, q=torch.zeros(T, 8, 128, dtype=torch.bfloat16), page_table=torch.zeros(B, 4, **i32),
+                 sm_scale=0.1, out=torch.zeros(T, 8, 128, dtype=torch.bfloat16), lse_out=torch.zeros(T, 8))
+    layer.update(dict(k8_pool=pools[0], v8_pool=pools[1], k_scale=1.0, v_scale=1.0) if fp8 else
+                 dict(k_pool=pools[0], v_pool=pools[1]))
+    return plan, layer
+
+
+@pytest.mark.parametrize("name", ["seq_lens", "cu_seqlens_q", "parent"])
+def test_tree_plan_refuses_other_types_and_strides(lib, name):
+    """A tree built by torch.tensor of Python integers is 64-bit: its words would be read as another tree."""
+    plan, _ = attention_arguments()
+    t = plan[name]
+    bad = [t.to(torch.int64), t.to(torch.float32), torch.stack([t, t], -1)[..., 0]]
+    bad += [] if name == "parent" else [t[:-1]]
+    for x in bad:
+        with pytest.raises(ValueError, match=name):
+            pa.attn_plan_tree(**dict(plan, **{name: x}))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_attention_refuses_other_types_and_strides(lib, fp8):
+    _, layer = attention_arguments(fp8)
+    call = pa.attn_tree_paged_fp8 if fp8 else pa.attn_tree_paged
+    k, v = ("k8_pool", "v8_pool") if fp8 else ("k_pool", "v_pool")
+    wide = torch.zeros(6, 12, 128, dtype=torch.bfloat16)                       # queries inside a fused projection
+    bad = [("q", wide[:, :8]), ("out", wide[:, :8]), ("q", layer["q"].float()), ("out", layer["out"].half()),
+           ("lse_out", layer["lse_out"].double()), ("lse_out", torch.zeros(6, 12)[:, :8]),
+           ("page_table", layer["page_table"].long()), ("page_table", torch.zeros(2, 8, dtype=torch.int32)[:, :4]),
+           ("page_table", layer["page_table"][:1])]
+    for name in (k, v):
+        other = torch.bfloat16 if fp8 else torch.uint8
+        bad += [(name, layer[name].to(other)), (name, layer[name].float()), (name, layer[name].transpose(0, 1))]
+    for name, x in bad:
+        with pytest.raises(ValueError, match=name):
+            call(**dict(layer, **{name: x}))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_attention_takes_bit_patterns_and_a_given_pitch(lib, monkeypatch, fp8):
+    """Raw 16-bit patterns, torch's own E4M3 type, and a table inside longer rows with its pitch given."""
+    _, layer = attention_arguments(fp8)
+    seen = []
+
+    class Fake:
+        def attn_tree_paged(self, *args):
+            seen.append(args[8])
+            return pa.PA_OK
+
+        def attn_tree_paged_fp8(self, *args):
+            seen.append(args[10])
+            return pa.PA_OK
+
+    monkeypatch.setattr(pa._binding, "lib", lambda: Fake())
+    table = torch.zeros(2, 9, dtype=torch.int32)
+    layer.update(q=layer["q"].view(torch.int16), out=layer["out"].view(torch.uint16), page_table=table[:, 2:6], pt_pitch=9)
+    if fp8:
+        layer.update(k8_pool=layer["k8_pool"].view(torch.float8_e4m3fn), v8_pool=layer["v8_pool"].view(torch.int8))
+        pa.attn_tree_paged_fp8(**layer)
+    else:
+        layer.update(k_pool=layer["k_pool"].view(torch.int16))
+        pa.attn_tree_paged(**layer)
+    assert seen == [9]
