@@ -103,13 +103,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
-# the current stream's handle without the Stream object around it (a fifth of a small call's host time)
+# the current stream's handle without the Stream object around it, and whether there is a device at all without
+# asking the driver again (a fifth and a twentieth of a small call's host time)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_initialised = torch.cuda.is_initialized
 
 
 def _stream(stream):
     if stream is None:
-        if not torch.cuda.is_available():
+        if not _initialised() and not torch.cuda.is_available():
             return None
         return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
@@ -255,12 +257,15 @@ def attn_kv_store_sage(k8_new, v8_new, sf_k_new, out_cache_loc, k8_pool, v8_pool
     return _check(st, "attn_kv_store_sage", raise_on_error)
 
 
+_Tensor, _int32, _float32 = torch.Tensor, torch.int32, torch.float32
+
+
 def _vector(name, t, dtype, n=0):
     """Address of a dense tensor of at least n values of one type; an int is an address, None is NULL.  The kernels
     read 32-bit words: 64-bit tokens, as argmax and topk give them, would be taken for other tokens."""
-    if t is None or isinstance(t, int):
+    if type(t) is not _Tensor and (t is None or isinstance(t, int)):
         return t
-    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not dtype or (n and t.numel() < n) or not t.is_contiguous():
         raise ValueError(f"{name}: a dense {dtype} tensor of at least {n} values is needed")
     return t.data_ptr()
 
@@ -271,7 +276,7 @@ _BITS8 = frozenset((torch.uint8, torch.int8, torch.float8_e4m3fn))        # E4M3
 
 def _dense(name, t, kinds):
     """Address of a dense tensor of one of the given types (an int is an address, None is NULL)."""
-    if t is None or isinstance(t, int):
+    if type(t) is not _Tensor and (t is None or isinstance(t, int)):
         return t
     if t.dtype not in kinds or not t.is_contiguous():
         raise ValueError(f"{name}: a dense tensor of one of {sorted(map(str, kinds))} is needed")
@@ -282,7 +287,7 @@ def _table(page_table, batch, pt_pitch):
     """Address and pitch of a page table: dense, or columns of longer rows with their pitch given."""
     if pt_pitch is None:
         pt_pitch = page_table.shape[-1]
-        return _vector("page_table", page_table, torch.int32, batch * pt_pitch), int(pt_pitch)
+        return _vector("page_table", page_table, _int32, batch * pt_pitch), int(pt_pitch)
     if isinstance(page_table, torch.Tensor) and page_table.dtype is not torch.int32:
         raise ValueError("page_table: int32 is needed")
     return _ptr(page_table), int(pt_pitch)
@@ -290,9 +295,9 @@ def _table(page_table, batch, pt_pitch):
 
 def attn_plan_tree(params, seq_lens, cu_seqlens_q, parent, ws, stream=None, raise_on_error=True) -> int:
     """Plan of the draft-tree attention; parent int32 [sum n] (-1 a root, -2 a node not in use)."""
-    batch, i32 = params.batch, torch.int32
-    st = lib().attn_plan_tree(ctypes.byref(params), _vector("seq_lens", seq_lens, i32, batch),
-                              _vector("cu_seqlens_q", cu_seqlens_q, i32, batch + 1), _vector("parent", parent, i32),
+    batch = params.batch
+    st = lib().attn_plan_tree(ctypes.byref(params), _vector("seq_lens", seq_lens, _int32, batch),
+                              _vector("cu_seqlens_q", cu_seqlens_q, _int32, batch + 1), _vector("parent", parent, _int32),
                               _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     return _check(st, "attn_plan_tree", raise_on_error)
 
@@ -305,7 +310,7 @@ def attn_tree_paged(params, ws, q, k_pool, v_pool, page_table, sm_scale, out, ls
     st = lib().attn_tree_paged(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _dense("q", q, _BITS16),
                                _dense("k_pool", k_pool, _BITS16), _dense("v_pool", v_pool, _BITS16), int(num_slots),
                                table, pt_pitch, float(sm_scale), _dense("out", out, _BITS16),
-                               _vector("lse_out", lse_out, torch.float32), _stream(stream))
+                               _vector("lse_out", lse_out, _float32), _stream(stream))
     return _check(st, "attn_tree_paged", raise_on_error)
 
 
@@ -317,7 +322,7 @@ def attn_tree_paged_fp8(params, ws, q, k8_pool, v8_pool, k_scale, v_scale, page_
     st = lib().attn_tree_paged_fp8(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _dense("q", q, _BITS16),
                                    _dense("k8_pool", k8_pool, _BITS8), _dense("v8_pool", v8_pool, _BITS8),
                                    float(k_scale), float(v_scale), int(num_slots), table, pt_pitch, float(sm_scale),
-                                   _dense("out", out, _BITS16), _vector("lse_out", lse_out, torch.float32),
+                                   _dense("out", out, _BITS16), _vector("lse_out", lse_out, _float32),
                                    _stream(stream))
     return _check(st, "attn_tree_paged_fp8", raise_on_error)
 
@@ -332,21 +337,20 @@ def attn_tree_verify(cu_seqlens_q, parent, tokens, target_probs, draft_probs, u_
     vocab = target_probs.shape[-1] if vocab is None else vocab
     if min(t.shape[-1] for t in (target_probs, draft_probs) if t is not None) < vocab:
         raise ValueError("rows of probabilities shorter than the vocabulary")
-    i32, f32 = torch.int32, torch.float32
-    st = lib().attn_tree_verify(int(batch), int(rows), int(vocab), _vector("cu_seqlens_q", cu_seqlens_q, i32, batch + 1),
-                                _vector("parent", parent, i32), _vector("tokens", tokens, i32), _ptr(target_probs),
+    st = lib().attn_tree_verify(int(batch), int(rows), int(vocab), _vector("cu_seqlens_q", cu_seqlens_q, _int32, batch + 1),
+                                _vector("parent", parent, _int32), _vector("tokens", tokens, _int32), _ptr(target_probs),
                                 _row_pitch("target_probs", target_probs), _ptr(draft_probs),
                                 0 if draft_probs is None else _row_pitch("draft_probs", draft_probs),
-                                _vector("u_accept", u_accept, f32), _vector("u_final", u_final, f32, batch),
-                                _vector("accept_len", accept_len, i32), _ptr(accept_path),
-                                _path_width(accept_path, batch), _vector("next_token", next_token, i32, batch),
+                                _vector("u_accept", u_accept, _float32), _vector("u_final", u_final, _float32, batch),
+                                _vector("accept_len", accept_len, _int32), _ptr(accept_path),
+                                _path_width(accept_path, batch), _vector("next_token", next_token, _int32, batch),
                                 _ptr(ws), _stream(stream))
     return _check(st, "attn_tree_verify", raise_on_error)
 
 
 def _row_pitch(name, t) -> int:
     """Elements between the rows of an fp32 matrix whose rows are dense."""
-    if t.dtype is not torch.float32 or t.dim() != 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dtype is not _float32 or t.dim() != 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name}: a float32 matrix with dense rows is needed")
     return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[-1]))
 
@@ -354,7 +358,7 @@ def _row_pitch(name, t) -> int:
 def _path_width(path, batch) -> int:
     """Width of the accepted paths.  The kernels take it for the rows' stride too and fill rows to it, so the rows
     are dense: columns inside longer rows are refused."""
-    if path.dtype is not torch.int32 or path.dim() != 2 or path.shape[0] < batch or not path.is_contiguous():
+    if path.dtype is not _int32 or path.dim() != 2 or path.shape[0] < batch or not path.is_contiguous():
         raise ValueError("accept_path: a dense torch.int32 matrix with a row for each request is needed")
     return int(path.shape[1])
 
@@ -388,15 +392,14 @@ def attn_kv_compact(pool_list, seq_lens, cu_seqlens_q, accept_len, accept_path, 
     batch = accept_len.shape[0]
     # without a bound on the rows: what the batch can hold
     rows = 256 * batch if max_q_tokens is None else max_q_tokens
-    i32 = torch.int32
     table, pt_pitch = _table(page_table, batch, pt_pitch)
     st = lib().attn_kv_compact(pool_list.array, len(pool_list.pools), pool_list.hkv, pool_list.head_dim,
                                pool_list.elem_bytes, pool_list.num_slots, int(batch), int(rows),
-                               _vector("seq_lens", seq_lens, i32, batch),
-                               _vector("cu_seqlens_q", cu_seqlens_q, i32, batch + 1),
-                               _vector("accept_len", accept_len, i32), _ptr(accept_path),
+                               _vector("seq_lens", seq_lens, _int32, batch),
+                               _vector("cu_seqlens_q", cu_seqlens_q, _int32, batch + 1),
+                               _vector("accept_len", accept_len, _int32), _ptr(accept_path),
                                _path_width(accept_path, batch), table, pt_pitch, int(page_size),
-                               _vector("seq_lens_out", seq_lens_out, i32, batch), _ptr(ws), _stream(stream))
+                               _vector("seq_lens_out", seq_lens_out, _int32, batch), _ptr(ws), _stream(stream))
     return _check(st, "attn_kv_compact", raise_on_error)
 
 
