@@ -372,7 +372,9 @@ pa_status pa_noalloc_read_device_error(pa_stream_t stream);
  * Request r brings n_r = cu_seqlens_q[r + 1] - cu_seqlens_q[r] nodes, 0 <= n_r <= min(256, L_r),
  * whose K/V rows are already in the pool at positions p_r + i, p_r = L_r - n_r.
  *
- * d_seq_lens      int32 [B]: L_r, prefix plus nodes;  d_cu_seqlens_q int32 [B + 1].
+ * d_seq_lens      int32 [B]: L_r, prefix plus nodes;  d_cu_seqlens_q int32 [B + 1], which need not start
+ *                 at 0: rows before the first request's (other tokens of a mixed batch) are not looked at,
+ *                 but count for max_q_tokens, the bound on cu_seqlens_q[B].
  * d_parent        int32 [sum n]: the parent of each node, an index inside its request: -1 for a
  *                 root, -2 for a node that is not in use (the padding of a graph captured at a
  *                 fixed size), else an earlier node (parent < own index).  A node below an unused
@@ -406,7 +408,7 @@ pa_status attn_plan_tree(const pa_plan_params* params, const int32_t* d_seq_lens
  *
  * params, d_ws    the plan (mode PA_MODE_TREE); any page size 1 .. 256.
  * d_q, d_out      bf16 [sum n][Hq][D];  d_lse_out fp32 [sum n][Hq] or NULL.
- * Rows of Q behind the last request are not read, rows of O and lse not written.  Pools and table
+ * Rows of Q before the first and behind the last request are not read, rows of O and lse not written.  Pools and table
  * as for attn_decode_paged; num_slots < 2^31.  Two calls that overlap in time need a workspace
  * each (it holds the partial outputs); calls in one stream, or one captured graph, share one.
  */

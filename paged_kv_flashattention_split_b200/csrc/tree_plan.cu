@@ -107,11 +107,13 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanLaunch 
     my_units += tiles * ktiles;
   }
   // the parents, checked here so that only this block writes the error word; all loads at once, the scans
-  // hide them.  (With lengths out of range the search may find a wrong request: the error is there then.)
+  // hide them.  Rows before the first request's belong to something else.  (With offsets out of range the
+  // search may find a wrong request: the error is there then.)
   const int rows = max(0, min(a.cu_seqlens_q[B], a.max_q_tokens));
+  const int row0 = max(0, min(a.cu_seqlens_q[0], rows)) + tid;
   int parent[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) parent[k] = tid + k * nt < rows ? a.parent[tid + k * nt] : -1;
+  for (int k = 0; k < 4; ++k) parent[k] = row0 + k * nt < rows ? a.parent[row0 + k * nt] : -1;
   int total = 0;
   const int units0 = block_exclusive_scan(my_units, scan_units, &total);
   const int per = max(1, (int)(((long long)total + a.slots - 1) / a.slots));
@@ -157,8 +159,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanLaunch 
   };
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (tid + k * nt < rows) check(tid + k * nt, parent[k]);
-  for (int k = tid + 4 * nt; k < rows; k += nt) check(k, a.parent[k]);
+    if (row0 + k * nt < rows) check(row0 + k * nt, parent[k]);
+  for (int row = row0 + 4 * nt; row < rows; row += nt) check(row, a.parent[row]);
   __syncthreads();
   // slot_first[c] = first item whose slot is >= c (slots are non-decreasing along the list)
   for (int x = tid; x < n_items; x += nt) {

@@ -354,3 +354,27 @@ def test_rows_far_behind_four_gigabytes(fp8):
     c.table += (slots - c.slots) // 16
     for a, b in zip(want, c.run()):
         assert torch.equal(a.nan_to_num(nan=7.0), b.nan_to_num(nan=7.0))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("skip", [1, 3, 700])
+def test_tree_rows_behind_other_rows(skip, fp8):
+    """Offsets that start behind the rows of something else (prefill tokens of a mixed batch): no error is
+    recorded, nothing of those rows is read or written, and the results are the same bit for bit."""
+    sizes = [(300, 17), (0, 5), (40, 33)]
+    plain = Case(sizes, 8, 2, 16, fp8, unused=0.1, seed=61)
+    want, want_lse = plain.run()
+    c = Case(sizes, 8, 2, 16, fp8, unused=0.1, seed=61)
+    c.q = torch.cat([torch.full((skip, 8, 128), float("nan"), dtype=c.q.dtype, device=c.q.device), c.q])
+    c.parent = torch.cat([torch.tensor([7, -9, 1 << 30], dtype=torch.int32, device=c.q.device).repeat(skip)[:skip], c.parent])
+    c.cu += skip
+    out, lse = c.run(max_q_tokens=c.T + skip)                 # run() checks that no error was recorded
+    assert torch.all(torch.isnan(out[:skip])) and torch.all(torch.isnan(lse[:skip]))
+    for a, b in ((out[skip:], want), (lse[skip:], want_lse)):
+        assert torch.equal(a.nan_to_num(nan=7.0), b.nan_to_num(nan=7.0))
+    # a wrong parent is still found there
+    params = c.params(max_q_tokens=c.T + skip)
+    ws = alloc_ws(params)
+    c.parent[skip + c.T - 1] = 33
+    pa.attn_plan_tree(params, c.seq_lens, c.cu, c.parent, ws)
+    assert pa.pa_read_device_error(ws) == pa.PA_ERR_DEVICE_INDEX

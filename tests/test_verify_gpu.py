@@ -427,3 +427,35 @@ def test_probability_rows_far_behind_2_to_the_31():
     torch.cuda.synchronize()
     for a, b in zip(got, (n, path, nxt)):
         assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_a_step_whose_rows_start_behind_others():
+    """Verification and compaction with offsets that do not start at 0."""
+    skip = 37
+    for drafts in (True, False):
+        d = Drafts([6, 9, 1], 1001, drafts, seed=63)
+        want = d.run()
+        for name in ("target", "draft"):
+            rows = getattr(d, name)
+            if rows is not None:
+                setattr(d, name, np.concatenate([np.full((skip, 1001), np.nan, np.float32), rows]))
+        d.parent = np.concatenate([np.full(skip, 9, np.int32), d.parent])
+        d.tokens = np.concatenate([np.full(skip, -5, np.int32), d.tokens])
+        d.u_accept = np.concatenate([np.full(skip, np.nan, np.float32), d.u_accept])
+        d.cu = d.cu + np.int32(skip)
+        params = pa.make_params(pa.PA_MODE_DECODE, 1, 8, 8, 128, 1, max_kv_len=1)
+        ws = alloc_ws(params)
+        pa.attn_plan(params, torch.zeros(1, dtype=torch.int32, device=DEV), None, ws)
+        for a, b in zip(d.check(pitch=9, ws=ws), want):
+            assert np.array_equal(a, b)
+        assert pa.pa_read_device_error(ws) == pa.PA_OK
+    c, pools, path, length = compact_case([(20, 30), (9, 12)], 4, 2, 2, 1, 3)
+    want, lens = ot.kv_compact([raw(p) for p in pools], c.cu.cpu().numpy(), c.lens, length, path,
+                               c.table.cpu().numpy(), 4)
+    out = torch.zeros(2, dtype=torch.int32, device=DEV)
+    pa.attn_kv_compact(pa.make_pool_list(pools), c.seq_lens, c.cu + skip, torch.from_numpy(length).to(DEV),
+                       torch.from_numpy(path).to(DEV), c.table, 4, out, ws=ws, max_q_tokens=c.T + skip)
+    assert pa.pa_read_device_error(ws) == pa.PA_OK
+    assert np.array_equal(out.cpu().numpy(), lens)
+    for p, w in zip(pools, want):
+        assert np.array_equal(raw(p), w)
