@@ -420,8 +420,9 @@ pa_status attn_tree_paged(const pa_plan_params* params, const void* d_ws, size_t
 /*
  * attn_tree_paged_fp8 - the same over an FP8 cache: K = k_scale E4M3(K8), V = v_scale E4M3(V8),
  * with the pools of attn_decode_paged_fp8.  A row of Q may have any finite bf16 values; one that is
- * smaller than 2^-9 of its row's largest is taken to within 2^-17 of the largest.  The NaN codes
- * (0x7F, 0xFF) must not occur in rows of nodes in use or of the prefix: in V they read as +-480.
+ * smaller than 2^-9 of its row's largest is taken to within 2^-17 of the largest (to within 2^-136
+ * in a row whose largest is below 2^-119).  The NaN codes (0x7F, 0xFF) must not occur in rows of nodes
+ * in use or of the prefix: in V they read as +-480.
  */
 pa_status attn_tree_paged_fp8(const pa_plan_params* params, const void* d_ws, size_t ws_bytes, const uint16_t* d_q,
                               const uint8_t* d_k8_pool, const uint8_t* d_v8_pool, float k_scale, float v_scale,

@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
 #pragma unroll
           for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int e = max(-119, min(126, (int)(__float_as_uint(mx) >> 23) - 127));   // 2^e <= mx
+          const int e = max(-119, min(127, (int)(__float_as_uint(mx) >> 23) - 127));   // 2^e <= mx, above 2^-119
           const float up = mx < __int_as_float(0x7f800000) ? __int_as_float((127 + 7 - e) << 23) : __int_as_float(0x7fc00000);
           uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll

@@ -378,3 +378,32 @@ def test_tree_rows_behind_other_rows(skip, fp8):
     c.parent[skip + c.T - 1] = 33
     pa.attn_plan_tree(params, c.seq_lens, c.cu, c.parent, ws)
     assert pa.pa_read_device_error(ws) == pa.PA_ERR_DEVICE_INDEX
+
+
+def test_queries_at_the_top_of_bf16_over_an_fp8_cache():
+    """Rows whose largest value is 2^127 or more keep the promised 2^-17 of it.  Subnormal key codes and small scales
+    bring the scores to a few units."""
+    c = Case([(300, 24), (20, 9)], 8, 2, 16, True, seed=62, scale=2.0 ** -62)
+    c.ks = 2.0 ** -60
+    g = torch.Generator(device="cuda").manual_seed(2)
+    live = c.k != 0x7F
+    code = torch.randint(1, 8, (int(live.sum()),), generator=g, device="cuda")
+    sign = 128 * torch.randint(0, 2, (int(live.sum()),), generator=g, device="cuda")
+    c.k[live] = (code + sign).to(torch.uint8)
+
+    def values(lo, hi):
+        x = lo + (hi - lo) * torch.rand(c.q.shape, generator=g, device="cuda")
+        return x * (1 - 2 * torch.randint(0, 2, c.q.shape, generator=g, device="cuda"))
+
+    def load(x, exponent):
+        c.q.copy_((x.to(torch.bfloat16).float() * 2.0 ** exponent).to(torch.bfloat16))
+        assert torch.all(torch.isfinite(c.q.float()))
+
+    load(values(1.75, 1.98), 127)                             # 8 significant bits in the upper quarter of the binade
+    c.check(*c.run(), "top")
+    x = values(1.0, 1.98)
+    x[:, :, 1::2] *= 2.0 ** -9                                # one part of the row at the split's lower end
+    load(x, 127)
+    c.check(*c.run(), "top and 2^-9 of it")
+    load(values(1.0, 1.98), 126)
+    c.check(*c.run(), "2^126")
