@@ -59,11 +59,11 @@ struct Shared {
 
 __device__ __forceinline__ double positive(float p) { return p > 0.f ? (double)p : 0.0; }   // a NaN counts as 0
 
-// A probability as a double, exactly (one below the normal range, 2^-126, as 0): the fields moved by
-// integer operations, beside the conversions of the other row, which run at a quarter of their rate.
+// A probability as a double, exactly (one below the normal range, 2^-126, as 0, and so is -0): the fields moved
+// by integer operations, beside the conversions of the other row, which run at a quarter of their rate.
 __device__ __forceinline__ double by_bits(float q) {
   const uint32_t b = __float_as_uint(q);
-  return __hiloint2double(b >= 0x00800000u ? (int)((b >> 3) + ((1023u - 127u) << 20)) : 0, (int)(b << 29));
+  return __hiloint2double((int)b >= 0x00800000 ? (int)((b >> 3) + ((1023u - 127u) << 20)) : 0, (int)(b << 29));
 }
 
 // The weights of the current node's row, taken through the rejections so far.

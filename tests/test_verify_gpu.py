@@ -429,6 +429,21 @@ def test_probability_rows_far_behind_2_to_the_31():
         assert np.array_equal(a.cpu().numpy(), b)
 
 
+@pytest.mark.parametrize("zero", [0.0, -0.0])
+def test_draft_probabilities_of_either_zero(zero):
+    """A draft probability of zero, of either sign, leaves the token's weight as it is."""
+    for seed in range(6):
+        d = Drafts([3, 9, 5], 700, True, seed=seed, near=4.0, temp=1.0)
+        d.draft[:, ::3] = zero
+        d.u_accept[:] = 0.999
+        d.check()
+    # the only weight that a rejection leaves lies on such tokens
+    d = Drafts([2], 700, True, "chain", seed=9)
+    d.target[0], d.draft[0] = 0, zero
+    d.target[0, 5], d.target[0, 600], d.draft[0, 5], d.tokens[1], d.u_accept[1] = 0.25, 0.75, 1.0, 5, 0.5
+    assert d.check()[2][0] == 600
+
+
 def test_a_step_whose_rows_start_behind_others():
     """Verification and compaction with offsets that do not start at 0."""
     skip = 37
