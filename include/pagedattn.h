@@ -472,9 +472,10 @@ pa_status attn_tree_verify(int32_t batch, int32_t max_q_tokens, int32_t vocab, c
  * node 0 and the accepted nodes: seq_lens_out[r] = p_r + 1 + accept_len[r] (p_r for a request
  * whose path starts with -1, L_r for one without nodes).
  *
- * pools           HOST array of n_pools (<= 256) distinct device pointers, read during the call:
+ * pools           HOST array of n_pools (<= 256) device pointers, read during the call:
  *                 K and V pools [num_slots][Hkv][D] of elem_bytes (2: bf16, 1: FP8) a value,
- *                 16-byte aligned.  Not for Sage pools, whose rows belong to their block's scale.
+ *                 16-byte aligned, that do not overlap (else PA_ERR_INVALID).  Not for Sage pools,
+ *                 whose rows belong to their block's scale.
  * d_seq_lens, d_cu_seqlens_q, d_page_table [B][pt_pitch], page_size: as planned;
  * d_accept_len, d_accept_path [B][path_pitch]: from attn_tree_verify (path[k] >= k).
  * d_seq_lens_out  int32 [B] or NULL; not the memory of another argument.

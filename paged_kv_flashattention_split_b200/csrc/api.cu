@@ -574,11 +574,14 @@ pa_status attn_kv_compact(void* const* pools, int32_t n_pools, int32_t hkv, int3
     a.pools[i] = pools[i];
   }
   std::sort(a.pools, a.pools + n_pools, std::less<void*>());   // every pool is treated alike
-  if (std::adjacent_find(a.pools, a.pools + n_pools) != a.pools + n_pools) return PA_ERR_INVALID;   // rows would move twice
+  a.row_bytes = hkv * head_dim * elem_bytes;
+  for (int i = 1; i < n_pools; ++i)                            // rows that two pools share would move twice
+    if (reinterpret_cast<uintptr_t>(a.pools[i]) - reinterpret_cast<uintptr_t>(a.pools[i - 1]) <
+        (uint64_t)num_slots * (uint64_t)a.row_bytes)
+      return PA_ERR_INVALID;
   pa_status st = check_arch();
   if (st != PA_OK) return st;
   a.n_pools = n_pools;
-  a.row_bytes = hkv * head_dim * elem_bytes;
   a.batch = batch;
   a.page_shift = ilog2(page_size);
   a.max_q_tokens = max_q_tokens;

@@ -383,3 +383,20 @@ def test_tree_attention_takes_bit_patterns_and_a_given_pitch(lib, monkeypatch, f
         layer.update(k_pool=layer["k_pool"].view(torch.int16))
         pa.attn_tree_paged(**layer)
     assert seen == [9]
+
+
+def test_compaction_refuses_pools_that_overlap(lib, monkeypatch):
+    """Rows in two pools of a list would move twice, in no order."""
+    monkeypatch.setenv("PAGEDATTN_TEST_FORCE_ARCH", "90")          # what is accepted ends before a launch
+    row, slots = 2 * 128 * 2, 100
+
+    def compact(*pools):
+        return lib.attn_kv_compact((ctypes.c_void_p * len(pools))(*pools), len(pools), 2, 128, 2, slots, 2, 8, 16, 16, 16,
+                                   16, 4, 16, 4, 16, None, None, None)
+
+    a = 1 << 30
+    for other in (a, a + 16, a + (slots - 1) * row, a + slots * row - 16, a - 16, a - slots * row + 16):
+        assert compact(a, other) == INVALID
+        assert compact(a + 4 * slots * row, a, a + 2 * slots * row, other) == INVALID
+    for other in (a + slots * row, a - slots * row, a + 9 * slots * row):
+        assert compact(a, other) in (pa.PA_ERR_ARCH, pa.PA_ERR_CUDA)
