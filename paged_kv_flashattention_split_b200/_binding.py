@@ -390,8 +390,8 @@ def attn_kv_compact(pool_list, seq_lens, cu_seqlens_q, accept_len, accept_path, 
     """Move the accepted nodes' rows behind the prefixes, in every pool of pool_list (make_pool_list);
     accept_path as attn_tree_verify writes it ([B, width], dense)."""
     batch = accept_len.shape[0]
-    # without a bound on the rows: what the batch can hold
-    rows = 256 * batch if max_q_tokens is None else max_q_tokens
+    # only the offsets are held against the bound on the rows, so none is needed
+    rows = 2 ** 31 - 1 if max_q_tokens is None else max_q_tokens
     table, pt_pitch = _table(page_table, batch, pt_pitch)
     st = lib().attn_kv_compact(pool_list.array, len(pool_list.pools), pool_list.hkv, pool_list.head_dim,
                                pool_list.elem_bytes, pool_list.num_slots, int(batch), int(rows),

@@ -474,3 +474,20 @@ def test_a_step_whose_rows_start_behind_others():
     assert np.array_equal(out.cpu().numpy(), lens)
     for p, w in zip(pools, want):
         assert np.array_equal(raw(p), w)
+
+
+def test_compaction_needs_no_bound_on_the_rows():
+    """Offsets far behind other rows (a long prefill in the same batch), without max_q_tokens."""
+    c, pools, path, length = compact_case([(20, 30), (9, 12)], 4, 2, 2, 1, 5)
+    length[:], path[:] = 0, -1
+    for r, walk in enumerate(([0, 2, 17, 29], [0, 11])):
+        path[r, :len(walk)], length[r] = walk, len(walk) - 1
+    want, lens = ot.kv_compact([raw(p) for p in pools], c.cu.cpu().numpy(), c.lens, length, path,
+                               c.table.cpu().numpy(), 4)
+    out = torch.zeros(2, dtype=torch.int32, device=DEV)
+    pa.attn_kv_compact(pa.make_pool_list(pools), c.seq_lens, c.cu + 100000, torch.from_numpy(length).to(DEV),
+                       torch.from_numpy(path).to(DEV), c.table, 4, out)
+    torch.cuda.synchronize()
+    assert np.array_equal(out.cpu().numpy(), lens)
+    for p, w in zip(pools, want):
+        assert np.array_equal(raw(p), w)
