@@ -260,45 +260,84 @@ def attn_kv_store_sage(k8_new, v8_new, sf_k_new, out_cache_loc, k8_pool, v8_pool
 _Tensor, _int32, _float32 = torch.Tensor, torch.int32, torch.float32
 
 
-def _vector(name, t, dtype, n=0):
-    """Address of a dense tensor of at least n values of one type; an int is an address, None is NULL.  The kernels
-    read 32-bit words: 64-bit tokens, as argmax and topk give them, would be taken for other tokens."""
+def _here() -> int:
+    """Index of the current device, -1 without one (as a host tensor's get_device)."""
+    if _initialised() or torch.cuda.is_available():
+        return torch.cuda.current_device()
+    return -1
+
+
+def _stream_of(here, stream):
+    """The stream's handle; the current one of the current device if none is given."""
+    if stream is None and _raw_stream is not None and here >= 0:
+        return _raw_stream(here)
+    return _stream(stream)
+
+
+def _elsewhere(name, t):
+    """A tensor that is not on the current device: pinned host memory is within its reach, all else would fault."""
+    if t.device.type != "cpu" or not t.is_pinned():
+        raise ValueError(f"{name}: on {t.device}, not on the current device")
+
+
+def _vector(name, t, dtype, here, n=0):
+    """Address of a dense tensor of at least n values of one type on device `here`; an int is an address, None is NULL.
+    The kernels read 32-bit words: 64-bit tokens, as argmax and topk give them, would be taken for other tokens."""
     if type(t) is not _Tensor and (t is None or isinstance(t, int)):
         return t
     if t.dtype is not dtype or (n and t.numel() < n) or not t.is_contiguous():
         raise ValueError(f"{name}: a dense {dtype} tensor of at least {n} values is needed")
+    if t.get_device() != here:
+        _elsewhere(name, t)
     return t.data_ptr()
+
+
+def _workspace(ws, here):
+    """Address of a plan workspace."""
+    if type(ws) is not _Tensor and (ws is None or isinstance(ws, int)):
+        return ws
+    if not ws.is_contiguous():
+        raise ValueError("ws: a dense tensor is needed")
+    if ws.get_device() != here:
+        _elsewhere("ws", ws)
+    return ws.data_ptr()
 
 
 _BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))          # bf16, or its bit patterns
 _BITS8 = frozenset((torch.uint8, torch.int8, torch.float8_e4m3fn))        # E4M3 codes
 
 
-def _dense(name, t, kinds):
-    """Address of a dense tensor of one of the given types (an int is an address, None is NULL)."""
+def _dense(name, t, kinds, here):
+    """Address of a dense tensor of one of the given types on device `here` (an int is an address, None is NULL)."""
     if type(t) is not _Tensor and (t is None or isinstance(t, int)):
         return t
     if t.dtype not in kinds or not t.is_contiguous():
         raise ValueError(f"{name}: a dense tensor of one of {sorted(map(str, kinds))} is needed")
+    if t.get_device() != here:
+        _elsewhere(name, t)
     return t.data_ptr()
 
 
-def _table(page_table, batch, pt_pitch):
+def _table(page_table, batch, pt_pitch, here):
     """Address and pitch of a page table: dense, or columns of longer rows with their pitch given."""
     if pt_pitch is None:
         pt_pitch = page_table.shape[-1]
-        return _vector("page_table", page_table, _int32, batch * pt_pitch), int(pt_pitch)
-    if isinstance(page_table, torch.Tensor) and page_table.dtype is not torch.int32:
-        raise ValueError("page_table: int32 is needed")
+        return _vector("page_table", page_table, _int32, here, batch * pt_pitch), int(pt_pitch)
+    if isinstance(page_table, _Tensor):
+        if page_table.dtype is not _int32:
+            raise ValueError("page_table: int32 is needed")
+        if page_table.get_device() != here:
+            _elsewhere("page_table", page_table)
     return _ptr(page_table), int(pt_pitch)
 
 
 def attn_plan_tree(params, seq_lens, cu_seqlens_q, parent, ws, stream=None, raise_on_error=True) -> int:
     """Plan of the draft-tree attention; parent int32 [sum n] (-1 a root, -2 a node not in use)."""
-    batch = params.batch
-    st = lib().attn_plan_tree(ctypes.byref(params), _vector("seq_lens", seq_lens, _int32, batch),
-                              _vector("cu_seqlens_q", cu_seqlens_q, _int32, batch + 1), _vector("parent", parent, _int32),
-                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    batch, here = params.batch, _here()
+    st = lib().attn_plan_tree(ctypes.byref(params), _vector("seq_lens", seq_lens, _int32, here, batch),
+                              _vector("cu_seqlens_q", cu_seqlens_q, _int32, here, batch + 1),
+                              _vector("parent", parent, _int32, here), _workspace(ws, here),
+                              ws.numel() * ws.element_size(), _stream_of(here, stream))
     return _check(st, "attn_plan_tree", raise_on_error)
 
 
@@ -306,11 +345,13 @@ def attn_tree_paged(params, ws, q, k_pool, v_pool, page_table, sm_scale, out, ls
                     pt_pitch=None, stream=None, raise_on_error=True) -> int:
     """Draft-tree attention for one layer over a TREE plan; q and out bf16 [sum n, Hq, D]."""
     num_slots = k_pool.shape[0] if num_slots is None else num_slots
-    table, pt_pitch = _table(page_table, params.batch, pt_pitch)
-    st = lib().attn_tree_paged(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _dense("q", q, _BITS16),
-                               _dense("k_pool", k_pool, _BITS16), _dense("v_pool", v_pool, _BITS16), int(num_slots),
-                               table, pt_pitch, float(sm_scale), _dense("out", out, _BITS16),
-                               _vector("lse_out", lse_out, _float32), _stream(stream))
+    here = _here()
+    table, pt_pitch = _table(page_table, params.batch, pt_pitch, here)
+    st = lib().attn_tree_paged(ctypes.byref(params), _workspace(ws, here), ws.numel() * ws.element_size(),
+                               _dense("q", q, _BITS16, here), _dense("k_pool", k_pool, _BITS16, here),
+                               _dense("v_pool", v_pool, _BITS16, here), int(num_slots), table, pt_pitch,
+                               float(sm_scale), _dense("out", out, _BITS16, here),
+                               _vector("lse_out", lse_out, _float32, here), _stream_of(here, stream))
     return _check(st, "attn_tree_paged", raise_on_error)
 
 
@@ -318,12 +359,14 @@ def attn_tree_paged_fp8(params, ws, q, k8_pool, v8_pool, k_scale, v_scale, page_
                         num_slots=None, pt_pitch=None, stream=None, raise_on_error=True) -> int:
     """Draft-tree attention over E4M3 pools (uint8 codes) dequantised by k_scale / v_scale; q and out bf16."""
     num_slots = k8_pool.shape[0] if num_slots is None else num_slots
-    table, pt_pitch = _table(page_table, params.batch, pt_pitch)
-    st = lib().attn_tree_paged_fp8(ctypes.byref(params), _ptr(ws), ws.numel() * ws.element_size(), _dense("q", q, _BITS16),
-                                   _dense("k8_pool", k8_pool, _BITS8), _dense("v8_pool", v8_pool, _BITS8),
-                                   float(k_scale), float(v_scale), int(num_slots), table, pt_pitch, float(sm_scale),
-                                   _dense("out", out, _BITS16), _vector("lse_out", lse_out, _float32),
-                                   _stream(stream))
+    here = _here()
+    table, pt_pitch = _table(page_table, params.batch, pt_pitch, here)
+    st = lib().attn_tree_paged_fp8(ctypes.byref(params), _workspace(ws, here), ws.numel() * ws.element_size(),
+                                   _dense("q", q, _BITS16, here), _dense("k8_pool", k8_pool, _BITS8, here),
+                                   _dense("v8_pool", v8_pool, _BITS8, here), float(k_scale), float(v_scale),
+                                   int(num_slots), table, pt_pitch, float(sm_scale),
+                                   _dense("out", out, _BITS16, here), _vector("lse_out", lse_out, _float32, here),
+                                   _stream_of(here, stream))
     return _check(st, "attn_tree_paged_fp8", raise_on_error)
 
 
@@ -337,30 +380,38 @@ def attn_tree_verify(cu_seqlens_q, parent, tokens, target_probs, draft_probs, u_
     vocab = target_probs.shape[-1] if vocab is None else vocab
     if min(t.shape[-1] for t in (target_probs, draft_probs) if t is not None) < vocab:
         raise ValueError("rows of probabilities shorter than the vocabulary")
-    st = lib().attn_tree_verify(int(batch), int(rows), int(vocab), _vector("cu_seqlens_q", cu_seqlens_q, _int32, batch + 1),
-                                _vector("parent", parent, _int32), _vector("tokens", tokens, _int32), _ptr(target_probs),
-                                _row_pitch("target_probs", target_probs), _ptr(draft_probs),
-                                0 if draft_probs is None else _row_pitch("draft_probs", draft_probs),
-                                _vector("u_accept", u_accept, _float32), _vector("u_final", u_final, _float32, batch),
-                                _vector("accept_len", accept_len, _int32), _ptr(accept_path),
-                                _path_width(accept_path, batch), _vector("next_token", next_token, _int32, batch),
-                                _ptr(ws), _stream(stream))
+    here = _here()
+    st = lib().attn_tree_verify(int(batch), int(rows), int(vocab),
+                                _vector("cu_seqlens_q", cu_seqlens_q, _int32, here, batch + 1),
+                                _vector("parent", parent, _int32, here), _vector("tokens", tokens, _int32, here),
+                                *_rows("target_probs", target_probs, here), *_rows("draft_probs", draft_probs, here),
+                                _vector("u_accept", u_accept, _float32, here),
+                                _vector("u_final", u_final, _float32, here, batch),
+                                _vector("accept_len", accept_len, _int32, here), *_paths(accept_path, batch, here),
+                                _vector("next_token", next_token, _int32, here, batch), _workspace(ws, here),
+                                _stream_of(here, stream))
     return _check(st, "attn_tree_verify", raise_on_error)
 
 
-def _row_pitch(name, t) -> int:
-    """Elements between the rows of an fp32 matrix whose rows are dense."""
+def _rows(name, t, here):
+    """Address of an fp32 matrix whose rows are dense, and the values between its rows; None is NULL."""
+    if t is None:
+        return None, 0
     if t.dtype is not _float32 or t.dim() != 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name}: a float32 matrix with dense rows is needed")
-    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[-1]))
+    if t.get_device() != here:
+        _elsewhere(name, t)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[-1])
 
 
-def _path_width(path, batch) -> int:
-    """Width of the accepted paths.  The kernels take it for the rows' stride too and fill rows to it, so the rows
-    are dense: columns inside longer rows are refused."""
+def _paths(path, batch, here):
+    """Address and width of the accepted paths.  The kernels take the width for the rows' stride too and fill rows to
+    it, so the rows are dense: columns inside longer rows are refused."""
     if path.dtype is not _int32 or path.dim() != 2 or path.shape[0] < batch or not path.is_contiguous():
         raise ValueError("accept_path: a dense torch.int32 matrix with a row for each request is needed")
-    return int(path.shape[1])
+    if path.get_device() != here:
+        _elsewhere("accept_path", path)
+    return path.data_ptr(), path.shape[1]
 
 
 class PoolList:
@@ -376,6 +427,9 @@ class PoolList:
         for p in self.pools:
             if p.shape != first.shape or p.element_size() != self.elem_bytes or not p.is_contiguous():
                 raise ValueError("the pools of a list are contiguous and of one shape and item size")
+            if p.device != first.device:
+                raise ValueError("the pools of a list are on one device")
+        self.device = first.get_device()
         self.array = (_P * len(self.pools))(*[p.data_ptr() for p in self.pools])
 
 
@@ -392,14 +446,18 @@ def attn_kv_compact(pool_list, seq_lens, cu_seqlens_q, accept_len, accept_path, 
     batch = accept_len.shape[0]
     # only the offsets are held against the bound on the rows, so none is needed
     rows = 2 ** 31 - 1 if max_q_tokens is None else max_q_tokens
-    table, pt_pitch = _table(page_table, batch, pt_pitch)
+    here = _here()
+    if pool_list.device != here:
+        _elsewhere("pools", pool_list.pools[0])
+    table, pt_pitch = _table(page_table, batch, pt_pitch, here)
     st = lib().attn_kv_compact(pool_list.array, len(pool_list.pools), pool_list.hkv, pool_list.head_dim,
                                pool_list.elem_bytes, pool_list.num_slots, int(batch), int(rows),
-                               _vector("seq_lens", seq_lens, _int32, batch),
-                               _vector("cu_seqlens_q", cu_seqlens_q, _int32, batch + 1),
-                               _vector("accept_len", accept_len, _int32), _ptr(accept_path),
-                               _path_width(accept_path, batch), table, pt_pitch, int(page_size),
-                               _vector("seq_lens_out", seq_lens_out, _int32, batch), _ptr(ws), _stream(stream))
+                               _vector("seq_lens", seq_lens, _int32, here, batch),
+                               _vector("cu_seqlens_q", cu_seqlens_q, _int32, here, batch + 1),
+                               _vector("accept_len", accept_len, _int32, here), *_paths(accept_path, batch, here),
+                               table, pt_pitch, int(page_size),
+                               _vector("seq_lens_out", seq_lens_out, _int32, here, batch), _workspace(ws, here),
+                               _stream_of(here, stream))
     return _check(st, "attn_kv_compact", raise_on_error)
 
 

@@ -400,3 +400,33 @@ def test_compaction_refuses_pools_that_overlap(lib, monkeypatch):
         assert compact(a + 4 * slots * row, a, a + 2 * slots * row, other) == INVALID
     for other in (a + slots * row, a - slots * row, a + 9 * slots * row):
         assert compact(a, other) in (pa.PA_ERR_ARCH, pa.PA_ERR_CUDA)
+
+
+def test_host_tensors_are_refused_where_there_is_a_device(lib, monkeypatch):
+    """A tree built on the host and forgotten there is refused, not read by the kernel; pinned memory is in reach."""
+    calls = []
+
+    class Fake:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(name) or pa.PA_OK
+
+    monkeypatch.setattr(pa._binding, "lib", lambda: Fake())
+    monkeypatch.setattr(pa._binding, "_stream_of", lambda here, stream: None)
+    plan, layer = attention_arguments()
+    _, layer8 = attention_arguments(fp8=True)
+    verify, compact = step_arguments()
+    for call, args in ((pa.attn_plan_tree, plan), (pa.attn_tree_paged, layer), (pa.attn_tree_paged_fp8, layer8),
+                       (pa.attn_tree_verify, verify), (pa.attn_kv_compact, compact)):
+        monkeypatch.setattr(pa._binding, "_here", lambda: -1)
+        call(**args)                                               # host tensors, no device: the library answers
+        monkeypatch.setattr(pa._binding, "_here", lambda: 0)
+        for name in [k for k, v in args.items() if isinstance(v, (torch.Tensor, pa._binding.PoolList))]:
+            # all other tensors count as pinned
+            monkeypatch.setattr(pa._binding, "_elsewhere",
+                                lambda n, t, name=name: elsewhere(n, t) if n == name.replace("pool_list", "pools") else None)
+            with pytest.raises(ValueError, match="not on the current device"):
+                call(**args)
+    assert calls == ["attn_plan_tree", "attn_tree_paged", "attn_tree_paged_fp8", "attn_tree_verify", "attn_kv_compact"]
+
+
+elsewhere = pa._binding._elsewhere

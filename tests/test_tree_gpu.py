@@ -407,3 +407,18 @@ def test_queries_at_the_top_of_bf16_over_an_fp8_cache():
     c.check(*c.run(), "top and 2^-9 of it")
     load(values(1.0, 1.98), 126)
     c.check(*c.run(), "2^126")
+
+
+def test_host_tensors():
+    """Pinned host memory is within the kernel's reach; other host memory is refused before a launch."""
+    c = Case([(100, 8), (33, 5)], 8, 2, 16, seed=64)
+    want, _ = c.run()
+    for name in ("seq_lens", "cu", "parent"):
+        setattr(c, name, getattr(c, name).cpu().pin_memory())
+    out, lse = c.run()
+    assert torch.equal(out.nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+    for name in ("seq_lens", "cu", "parent", "q", "k", "table"):
+        d = Case([(100, 8), (33, 5)], 8, 2, 16, seed=64)
+        setattr(d, name, getattr(d, name).cpu())
+        with pytest.raises(ValueError, match="current device"):
+            d.run()
