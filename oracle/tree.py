@@ -129,3 +129,46 @@ def kv_compact(pools, cu_seqlens_q, seq_lens, accept_len, path, page_table, page
             p[slots[prefix + k]] = p[slots[prefix + path[r, k]]]
         lens[r] = prefix + 1 + int(accept_len[r])
     return pools, lens
+
+
+def plan_tree(seq_lens, cu_seqlens_q, parent, hq, hkv, max_kv_len, max_q_tokens, num_sms):
+    """The plan's arrays as attn_plan_tree documents them, for requests in range; a request out of range
+    (more keys than max_kv_len, more nodes than keys or than 256, rows outside max_q_tokens) has no work.
+
+    Returns a dict: tiles, base (units before each request, then all), prefix, items (r, tile, first key tile,
+    end key tile), slot_first, cut (query tiles cut into pieces), per, slots, bits (one row of 8 words a node).
+    """
+    B, nodes = len(seq_lens), 256 // (hq // hkv)
+    slots = max(1, num_sms // hkv)
+    cu = [int(x) for x in cu_seqlens_q]
+    tiles, ktiles, prefix = [], [], []
+    bits = np.zeros((max_q_tokens, 8), dtype=np.uint32)
+    for r in range(B):
+        L, n = int(seq_lens[r]), cu[r + 1] - cu[r]
+        if not (0 <= L <= max_kv_len and 0 <= cu[r] and cu[r + 1] <= max_q_tokens and 0 <= n <= min(L, 256)):
+            n = 0
+        tiles.append((n + nodes - 1) // nodes)
+        ktiles.append((L + 127) // 128 if n else 0)
+        prefix.append(L - n)
+        see = visibility(parent[cu[r]:cu[r] + n])
+        for i in range(n):
+            for j in np.flatnonzero(see[i]):
+                bits[cu[r] + i, j // 32] |= np.uint32(1) << np.uint32(j % 32)
+    base = [0]
+    for r in range(B):
+        base.append(base[-1] + tiles[r] * ktiles[r])
+    per = max(1, -(-base[-1] // slots))
+    items, item_slot, cut = [], [], []
+    for r in range(B):
+        for t in range(tiles[r]):
+            u0 = base[r] + t * ktiles[r]
+            owners = sorted({u // per for u in range(u0, u0 + ktiles[r])})
+            if len(owners) > 1:
+                cut.append((r, t))
+            for c in owners:
+                mine = [u for u in range(u0, u0 + ktiles[r]) if u // per == c]
+                items.append((r, t, mine[0] - u0, mine[-1] + 1 - u0))
+                item_slot.append(c)
+    slot_first = [sum(s < c for s in item_slot) for c in range(slots + 1)]
+    return dict(tiles=tiles, base=base, prefix=prefix, items=items, slot_first=slot_first, cut=cut, per=per, slots=slots,
+                bits=bits)

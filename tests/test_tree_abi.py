@@ -430,3 +430,133 @@ def test_host_tensors_are_refused_where_there_is_a_device(lib, monkeypatch):
 
 
 elsewhere = pa._binding._elsewhere
+
+
+# ------------------------------------------------------------------------------------- more pins of the oracle
+
+def bits_of(rng, *shape):
+    return (rng.standard_normal(shape).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+
+
+def test_one_node_is_the_decode():
+    rng = np.random.default_rng(4)
+    q, k, v = bits_of(rng, 3, 4, 128), bits_of(rng, 64, 2, 128), bits_of(rng, 64, 2, 128)
+    lens, table = np.array([20, 1, 32]), rng.permutation(16)[None, :8].repeat(3, 0)
+    o, lse, _ = ot.tree_attention(q, np.arange(4), [-1, -1, -1], k, v, table, lens, 4, 0.1)
+    ref, ref_lse = oa.decode(q, k, v, table, lens, 4, 0.1)
+    assert np.allclose(o, ref, atol=1e-13) and np.allclose(lse, ref_lse, atol=1e-13)
+
+
+def test_the_fp8_form_is_the_bf16_form_of_the_dequantised_cache():
+    """Scales that are powers of two: every dequantised value is a bf16 value."""
+    rng = np.random.default_rng(5)
+    codes = np.array([x for x in range(256) if x & 0x7F != 0x7F], dtype=np.uint8)
+    q = bits_of(rng, 9, 4, 128)
+    k8, v8 = rng.choice(codes, (64, 2, 128)), rng.choice(codes, (64, 2, 128))
+    table, lens, cu = rng.permutation(16).reshape(2, 8), np.array([20, 5]), np.array([0, 4, 9])
+    parent = [-1, 0, 0, 1, -1, -2, 0, 1, 2]
+    from oracle.codecs import e4m3_to_f64
+    as_bf16 = lambda c, s: ((e4m3_to_f64(c) * s).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)   # noqa: E731
+    a = ot.tree_attention(q, cu, parent, k8, v8, table, lens, 4, 0.01, 2.0 ** -4, 2.0 ** -6)
+    b = ot.tree_attention(q, cu, parent, as_bf16(k8, 2.0 ** -4), as_bf16(v8, 2.0 ** -6), table, lens, 4, 0.01)
+    for x, y in zip(a, b):
+        assert np.array_equal(np.isneginf(x), np.isneginf(y)) and np.allclose(x, y, atol=1e-13)
+
+
+def test_unused_nodes_give_and_change_nothing():
+    rng = np.random.default_rng(6)
+    q, k, v = bits_of(rng, 5, 2, 128), bits_of(rng, 16, 1, 128), bits_of(rng, 16, 1, 128)
+    args = ([0, 5], [-1, -2, 0, 1, 2], k, v, np.arange(16)[None], [12], 1, 0.1)      # node 3 hangs below node 1
+    o, lse, _ = ot.tree_attention(q, *args)
+    assert np.all(o[[1, 3]] == 0) and np.all(np.isneginf(lse[[1, 3]])) and np.all(np.isfinite(lse[[0, 2, 4]]))
+    for x in (k, v):
+        x[[8, 10]] = 0x7FC0                                                          # their rows: NaN
+    again, lse2, _ = ot.tree_attention(q, *args)
+    assert np.array_equal(o, again) and np.array_equal(lse, lse2)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_plan_invariants(seed):
+    """Every (query tile, key tile) unit once and in order, runs of at most `per` a slot, cut tiles listed."""
+    rng = np.random.default_rng(seed)
+    B, (hq, hkv) = int(rng.integers(1, 9)), [(8, 8), (8, 4), (16, 4), (32, 4)][seed % 4]
+    n = rng.integers(0, 60, B)
+    lens = n + rng.integers(0, 900, B)
+    cu = int(rng.integers(0, 5)) + np.concatenate([[0], np.cumsum(n)])
+    parent = [-2] * int(cu[0])
+    for k in n:
+        parent += [int(rng.integers(-2, i)) for i in range(int(k))]
+    p = ot.plan_tree(lens, cu, parent, hq, hkv, 2000, int(cu[-1]), int(rng.integers(1, 160)))
+    units = [(r, t, u) for r, t, a, b in p["items"] for u in range(a, b)]
+    nodes = 256 // (hq // hkv)
+    want = [(r, t, u) for r in range(B) for t in range(-(-int(n[r]) // nodes)) for u in range(-(-int(lens[r]) // 128))]
+    assert units == want and p["base"][-1] == len(want)
+    first = p["slot_first"]
+    assert first[0] == 0 and first[-1] == len(p["items"]) and len(first) == p["slots"] + 1
+    for a, b in zip(first, first[1:]):
+        assert a <= b and sum(i[3] - i[2] for i in p["items"][a:b]) <= p["per"]
+    pieces = [i[:2] for i in p["items"]]
+    assert p["cut"] == [x for x in dict.fromkeys(pieces) if pieces.count(x) > 1]
+    for r in range(B):
+        see = ot.visibility(parent[cu[r]:cu[r + 1]])
+        got = (p["bits"][cu[r]:cu[r + 1], :, None] >> np.arange(32)) & 1
+        assert np.array_equal(got.reshape(int(n[r]), 256)[:, :int(n[r])], see) and got.sum() == see.sum()
+
+
+def bisect_unit(f):
+    """Largest-but-eps u in [0, 1] with f(u) true, for an f that is true below a threshold."""
+    lo, hi = 0.0, 1.0
+    if not f(0.0):
+        return 0.0
+    if f(1.0 - 2.0 ** -53):
+        return 1.0
+    for _ in range(52):
+        mid = 0.5 * (lo + hi)
+        lo, hi = (mid, hi) if f(mid) else (lo, mid)
+    return hi
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("siblings", [1, 2, 3])
+def test_verification_enumerated(drafts, siblings):
+    """P(first token = x) = target(x), by enumeration: all drafted tokens with their probabilities under q, and the
+    random numbers integrated by finding the oracle's own thresholds.  Probabilities are multiples of 1/16."""
+    V = 3
+    p, q = np.array([8, 3, 5]) / 16, np.array([3, 9, 4]) / 16
+    rows = siblings + 1
+    target, draft = (np.tile(x.astype(np.float32), (rows, 1)) for x in (p, q))
+    cu, parent = [0, rows], [-1] + [0] * siblings
+
+    def walk(tokens, u_accept, u_final):
+        n, path, nxt = ot.verify(cu, parent, [0, *tokens], target, draft if drafts else None, np.array([0.0, *u_accept]),
+                                 np.array([u_final]), rows)
+        return (int(path[0, 1]) if n[0] else 0), int(nxt[0])
+
+    first = np.zeros(V)
+    cases = list(np.ndindex(*(V,) * siblings)) if drafts else [(2, 1, 0)[:siblings]]
+    for tokens in cases:
+        weight = np.prod(q[list(tokens)]) if drafts else 1.0
+        refused = []                                               # u = 1 is never below a ratio of at most 1
+        for c in range(siblings):
+            t = bisect_unit(lambda u: walk(tokens, refused + [u] + [1.0] * (siblings - c - 1), 0.0)[0] == c + 1)
+            first[tokens[c]] += weight * t
+            weight *= 1.0 - t
+            # a ratio above 1 accepts whatever u is: nothing is left then
+            refused.append(1.0)
+            if weight == 0.0:
+                break
+        if weight > 0.0:
+            edges = [0.0]
+            for x in range(V - 1):
+                edges.append(bisect_unit(lambda u: walk(tokens, refused, u)[1] <= x))
+            first += weight * np.diff(edges + [1.0])
+    assert np.allclose(first, p, atol=1e-12), (first, p)
+
+
+def test_accepted_tokens_lead_to_the_next_row():
+    """Two levels: after an accepted child the next token comes from that child's row."""
+    target = np.array([[0.5, 0.5, 0], [0, 0.25, 0.75], [1, 0, 0]], dtype=np.float32)
+    draft = np.tile(np.array([0.5, 0.25, 0.25], dtype=np.float32), (3, 1))
+    n, path, nxt = ot.verify([0, 3], [-1, 0, 1], [9, 1, 2], target, draft, np.array([0, 0.999, 0.999]), [0.5], 3)
+    # child 1 (token 1): 0.999 * 0.25 < 0.5; child 2 (token 2): 0.999 * 0.25 < 0.75; then row 2: token 0
+    assert n[0] == 2 and path[0].tolist() == [0, 1, 2] and nxt[0] == 0

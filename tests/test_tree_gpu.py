@@ -422,3 +422,101 @@ def test_host_tensors():
         setattr(d, name, getattr(d, name).cpu())
         with pytest.raises(ValueError, match="current device"):
             d.run()
+
+
+def read_tree_plan(ws, params):
+    """The workspace's arrays, from the layout documented at attn_plan_tree."""
+    raw, up = ws.cpu().numpy(), lambda x: -(-x // 256) * 256   # noqa: E731
+    hdr = raw[:64].view(np.int32)
+    B, at, out = params.batch, 64, {}
+
+    def take(n, dtype=np.int32):
+        nonlocal at
+        a = raw[at:at + 4 * n].view(dtype)
+        at += 4 * n
+        return a
+
+    for name, n in (("tiles", B), ("base", B + 1), ("lens", B), ("row0", B), ("prefix", B)):
+        out[name] = take(n)
+    at = -(-at // 16) * 16
+    out["items"] = take(4 * int(hdr[8])).reshape(-1, 4)[:hdr[7]]
+    at = up(at)
+    out["slot_first"] = take(int(hdr[14]) + 1)
+    at = up(at)
+    T = params.max_q_tokens // (256 // (params.hq // params.hkv)) + B
+    out["cut"] = take(2 * min(max(1, int(hdr[14]) - 1), T)).reshape(-1, 2)[:hdr[15]]
+    at = up(at)
+    out["bits"] = take(8 * params.max_q_tokens, np.uint32).reshape(-1, 8)
+    out.update(per=int(hdr[10]), slots=int(hdr[14]), header=hdr)
+    return out
+
+
+@pytest.mark.parametrize("batch,seed", [(b, s) for s in range(4) for b in (1, 2, 7, 33)] +
+                         [(256, 0), (257, 1), (1023, 2), (1025, 3), (3000, 4)])
+def test_plan_bit_exact(batch, seed):
+    """Every array of the plan against the oracle: both block sizes, several requests a thread, empty requests,
+    requests out of range, offsets behind other rows, plans for fewer SMs."""
+    import oracle.tree as ot
+    rng = np.random.default_rng(1000 * batch + seed)
+    hq, hkv = [(8, 8), (8, 4), (32, 8), (8, 1)][seed % 4]
+    n = rng.integers(0, 257 if batch < 40 else 6, batch)
+    n[rng.random(batch) < 0.2] = 0
+    lens = n + rng.integers(0, 3000 if batch < 40 else 200, batch)
+    cu = int(rng.integers(0, 40)) + np.concatenate([[0], np.cumsum(n)])
+    parent = [7] * int(cu[0])
+    for k in n:
+        parent += [int(rng.integers(max(-2, i - 5) if rng.random() < 0.9 else -2, i)) for i in range(int(k))]
+    bad = seed % 2 == 1
+    if bad:
+        lens[rng.random(batch) < 0.1] = 4000
+    rows, sms = int(cu[-1]) + int(rng.integers(1, 50)), int(rng.integers(1, 149))
+    params = pa.make_params(pa.PA_MODE_TREE, batch, hq, hkv, 128, 16, max_kv_len=3400, max_q_tokens=rows, num_sms=sms)
+    ws = alloc_ws(params)
+    ws.fill_(0)
+    t = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")   # noqa: E731
+    pa.attn_plan_tree(params, t(lens), t(cu), t(parent or [-1]), ws)
+    got = read_tree_plan(ws, params)
+    want = ot.plan_tree(lens, cu, parent, hq, hkv, 3400, rows, sms)
+    expect = pa.PA_ERR_DEVICE_INDEX if bad and np.any(lens == 4000) else pa.PA_OK
+    assert pa.pa_read_device_error(ws) == expect
+    assert (got["per"], got["slots"]) == (want["per"], want["slots"])
+    assert got["header"][1:7].tolist() == [pa.PA_MODE_TREE, batch, hq, hkv, 128, 16]
+    assert np.array_equal(got["lens"], lens) and np.array_equal(got["row0"], cu[:-1])
+    for name in ("tiles", "base", "prefix", "slot_first"):
+        assert np.array_equal(got[name], want[name]), name
+    for name, width in (("items", 4), ("cut", 2)):
+        assert np.array_equal(got[name], np.array(want[name], np.int32).reshape(-1, width)), name
+    assert np.array_equal(got["bits"], want["bits"])           # rows of nobody stay as they were
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [12, 40])
+@pytest.mark.parametrize("shape", ["lag", "stairs"])
+def test_large_values_behind_references_that_lag(shape, n, fp8):
+    """V up to 2^90 under weights near the top of what a row's reference allows: the keys that set the reference (the
+    first half of each stream's first tile) score just less below the others than what would raise it, over 4096 keys
+    of one slot; or the scores climb such a step every 512 keys.  Sums reach 2^16 x 4096 x 2^90 < 2^128."""
+    import oracle.tree as ot
+    lag = 7.9 if fp8 else 15.9
+    c = Case([(4096, n)], 4, 1, 16, fp8, seed=43)
+    if fp8:
+        c.vs = 2.0 ** 90 / 448
+    c.q[:] = 0.25                                             # q . k = 32 t for a key row of t's
+    c.scale = lag * np.log(2) / (32 * (c.ks or 1.0))
+    slots = torch.from_numpy(ot.gather_slots(c.table.cpu().numpy(), 4096, c.page, 0)).cuda()
+    pos = torch.arange(4096, device="cuda")
+    level = 1.0 + (pos // 512 if shape == "stairs" else 0 * pos)
+    level[(pos < 64) | ((pos >= 128) & (pos < 192))] = 0
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = level[:, None, None].expand(-1, 1, 128)
+    v = 0.5 + 0.5 * torch.rand(4096 + n, 1, 128, generator=g, device="cuda")
+    every = torch.from_numpy(ot.gather_slots(c.table.cpu().numpy(), 4096 + n, c.page, 0)).cuda()
+    if fp8:
+        c.k[slots] = k.to(torch.float8_e4m3fn).view(torch.uint8)
+        c.v[every] = (448 * v).to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        c.k[slots] = k.to(torch.bfloat16)
+        c.v[every] = (2.0 ** 90 * v).to(torch.bfloat16)
+    out, lse = c.run(num_sms=1)
+    assert torch.all(torch.isfinite(out[:c.T].float()))
+    c.check(out, lse, shape)

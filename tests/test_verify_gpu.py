@@ -491,3 +491,52 @@ def test_compaction_needs_no_bound_on_the_rows():
     assert np.array_equal(out.cpu().numpy(), lens)
     for p, w in zip(pools, want):
         assert np.array_equal(raw(p), w)
+
+
+class WideRows(Drafts):
+    """Few nodes over a long vocabulary, rows cheap to make: target and draft from uniform numbers."""
+
+    def __init__(self, counts, vocab, drafts, seed):
+        super().__init__(counts, 2, drafts, "chain", seed=seed)
+        rng = np.random.default_rng(seed)
+        self.vocab = vocab
+        self.target, draft = (rng.random((self.T, vocab), dtype=np.float32) for _ in range(2))
+        self.target /= self.target.sum(-1, keepdims=True)
+        draft /= draft.sum(-1, keepdims=True)
+        self.draft = draft if drafts else None
+        self.tokens = rng.integers(0, vocab, self.T).astype(np.int32)
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("counts,vocab", [
+    ([3, 2], 128256),                                          # 8 CTAs a request, 32 chunks of 512 tokens each
+    ([2] * 80, 128256),                                        # 4 CTAs, 63 chunks
+    ([1] * 310, 50001),                                        # 1 CTA, 98 chunks
+    ([2, 1], 1 << 20),                                         # 8 CTAs, 256 chunks
+])
+def test_long_vocabularies_in_many_chunks(counts, vocab, drafts):
+    """More chunks than warps and than lanes of the final search, drawn all along the vocabulary."""
+    d = WideRows(counts, vocab, drafts, seed=vocab % 1000 + len(counts))
+    d.u_final[:] = ((np.arange(d.B) + 0.5) / d.B).astype(np.float32)
+    d.check()
+    for u in (0.0, 0.03, 0.5, 0.97, 1 - 2.0 ** -24):
+        d.u_final[:] = np.float32(u)
+        d.check()
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("batch,vocab", [(2, 1 << 20), (3, (1 << 20) - 511), (310, 50001)])
+def test_weight_in_few_chunks_of_a_long_vocabulary(batch, vocab, drafts):
+    """All weight in the last chunk, or at single tokens of the first, a middle and the last chunk: the sums carried
+    over the chunks before have to be right."""
+    d = WideRows([1] * batch, vocab, drafts, seed=7)
+    d.target[:] = 0
+    d.target[:, -5:] = [0.25, 0, 0.25, 0.25, 0.25]
+    got = d.check()
+    assert np.all(got[2] >= vocab - 5)
+    d.target[:] = 0
+    at = [3, 511, 512, vocab // 2, vocab - 20000, vocab - 1]
+    d.target[:, at] = 1 / 6
+    for i, x in enumerate(at):
+        d.u_final[:] = np.float32((i + 0.5) / 6)
+        assert np.all(d.check()[2] == x)
