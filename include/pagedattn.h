@@ -404,7 +404,8 @@ pa_status attn_plan_tree(const pa_plan_params* params, const int32_t* d_seq_lens
  * A node that is not in use gives O = 0, lse = -inf, and its K/V rows may hold anything (NaN
  * included).  The K/V rows of nodes in use must be finite: a row of V that is not can reach
  * other nodes of its request.  Values of V up to 2^90 in size are safe: weights are held against a
- * row reference that a later key may pass by 2^16, and sums of larger values may overflow.
+ * row reference that a later key may pass by 2^16, and sums of larger values may overflow.  The
+ * weights that multiply V are rounded to bf16; their sum and lse take them unrounded, in fp32.
  *
  * params, d_ws    the plan (mode PA_MODE_TREE); any page size 1 .. 256.
  * d_q, d_out      bf16 [sum n][Hq][D];  d_lse_out fp32 [sum n][Hq] or NULL.
@@ -422,7 +423,8 @@ pa_status attn_tree_paged(const pa_plan_params* params, const void* d_ws, size_t
  * with the pools of attn_decode_paged_fp8.  A row of Q may have any finite bf16 values; one that is
  * smaller than 2^-9 of its row's largest is taken to within 2^-17 of the largest (to within 2^-136
  * in a row whose largest is below 2^-119).  The NaN codes (0x7F, 0xFF) must not occur in rows of nodes
- * in use or of the prefix: in V they read as +-480.
+ * in use or of the prefix: in V they read as +-480.  The weights that multiply V are rounded to f16:
+ * a key's share of its row's sum is taken to within 2^-11 of itself or 2^-31, whichever is more.
  */
 pa_status attn_tree_paged_fp8(const pa_plan_params* params, const void* d_ws, size_t ws_bytes, const uint16_t* d_q,
                               const uint8_t* d_k8_pool, const uint8_t* d_v8_pool, float k_scale, float v_scale,

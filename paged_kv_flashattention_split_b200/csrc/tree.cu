@@ -102,7 +102,8 @@ template <bool FP8> struct Cfg {
   static constexpr int kSmem = kSmall + kTiles;
   // P = 2^(x + kBias) with x a score's distance from the row's reference, which is raised when an x passes
   // kRaise.  bf16 has fp32's exponents: P <= 2^16, so sums over 2^17 keys of values up to 2^90 stay finite.
-  // f16 keeps P between 2^-24 and 2^16.
+  // f16 keeps P between 2^-24 and 2^16: below 2^-14 it is off by up to 2^-25, and a row's sum is at least 2^6 (the
+  // reference is less than 1 above the largest score it has seen), so a key's share by up to 2^-31.
   static constexpr float kBias = FP8 ? 7.f : 0.f, kRaise = FP8 ? 8.f : 16.f;
   // instruction descriptors: M 128, N 128, fp32 D; S: bf16 or E4M3, PV: bf16 or f16
   static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);

@@ -520,3 +520,29 @@ def test_large_values_behind_references_that_lag(shape, n, fp8):
     out, lse = c.run(num_sms=1)
     assert torch.all(torch.isfinite(out[:c.T].float()))
     c.check(out, lse, shape)
+
+
+def test_far_keys_under_a_peak_without_value_over_an_fp8_cache():
+    """A key that takes nearly all the weight and has V = 0: what is left of O are the far keys' shares, each taken to
+    within 2^-11 of itself or 2^-31 (the step of f16 at its lower end, 2^-25, over a row's sum of at least 2^6)."""
+    import oracle.tree as ot
+    for gap in (10.0, 16.0, 22.0, 40.0):
+        c = Case([(700, 9), (300, 40)], 8, 2, 16, True, seed=65, scale=gap / 32.0)
+        c.q[:] = 0.25                                         # q . k = 32 t for a key row of t's
+        table = c.table.cpu().numpy()
+        limit = []
+        for r in range(c.B):
+            slots = torch.from_numpy(ot.gather_slots(table, c.lens[r], c.page, r)).cuda()
+            c.k[slots] = 0
+            peak = slots[137]
+            c.k[peak] = int(torch.tensor(1.0 / c.ks).to(torch.float8_e4m3fn).view(torch.uint8))
+            c.v[peak] = 0
+            v = c.vs * c.v[slots].view(torch.float8_e4m3fn).double().abs().sum(0)             # [Hkv, D]
+            limit.append(v.repeat_interleave(4, 0).expand(c.n[r], -1, -1))
+        out, lse = c.run()
+        ref, ref_lse, mag = c.oracle()
+        err = np.abs(out[:c.T].double().cpu().numpy() - ref[:c.T])
+        tol = (2.0 ** -8 + 2.0 ** -11 + 2 * c.score_error() + 2.0 ** -16) * mag[:c.T]       # 2^-8: O in bf16
+        tol += 2.0 ** -31 * torch.cat(limit).cpu().numpy()
+        assert np.all(err <= tol), (gap, np.max(err / tol))
+        assert np.all(np.abs(lse[:c.T].cpu().numpy() - ref_lse[:c.T]) <= c.score_error() + 2.0 ** -16 + 2.0 ** -20 * np.abs(ref_lse[:c.T]))
