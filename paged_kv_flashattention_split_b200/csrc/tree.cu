@@ -10,9 +10,9 @@
 // slot's items (runs of 128-key tiles of one query tile):
 //   warps 0-3      gather K (0, 1) and V (2, 3) rows slot by slot with 16-byte cp.async into rings in
 //                  the tensor cores' 128-byte-swizzled layout: K by tiles of 128 keys, V by halves of
-//                  64.  Filling a ring this way measured 6.4-6.55 TB/s for pages of 8 slots and more
-//                  and 5.6 TB/s below, against 3.2-6.1 TB/s for one TMA box a page of 8 or 16 slots
-//                  and 6.8 TB/s at 64 and more, so one path serves every page size;
+//                  64.  Filling a ring this way, and nothing else, measured 6.4-6.55 TB/s for pages of 8
+//                  slots and more and 5.6 TB/s below, against 3.2-6.1 TB/s for one TMA box a page of 8 or
+//                  16 slots and 6.8 TB/s at 64 and more, so one path serves every page size;
 //   warp 4         issues the MMAs:  S_t = Q K^T,  O_t += P_t V  (M 128, N 128);
 //   warps 6, 7     fetch the item's Q rows;
 //   warps 8-15     two softmax warpgroups, one per stream t; thread = row.
@@ -26,7 +26,7 @@
 //
 // Softmax in one pass: a row's weights are 2^(score - ref) with a reference that is set by the first
 // keys it sees and raised only when a score passes it by far, so nothing waits for a tile's maximum
-// (8 requests of 128k tokens, 32 nodes, 64 heads: 1.23 ms, against 1.38 with the maximum first).
+// (8 requests of 128k tokens, 32 nodes, 64 heads, when it came in: 1.23 ms, against 1.38 with the maximum first).
 //
 // E4M3 pools.  K is used as it is: Q is split into two E4M3 terms whose sum is Q up to 2^-17 of its
 // row's largest value (hi = round(q 2^e), lo = round(q 2^e - hi), a power of two a row, so every bf16
@@ -38,12 +38,15 @@
 // Statistics are fp32.  P is rounded to bf16 (f16 for E4M3 pools) as the tensor cores need it; the
 // row sum adds the unrounded values, so lse does not see that rounding.
 //
-// What bounds it (cold L2, plan and merge included).  64 requests of 512-8192 tokens, up to 16 nodes,
-// 32 / 8 heads, page size 1: 215-231 us for 1.15 GB, 5.0-5.3 TB/s, the copies' rate at that page size.  8 x 128k
-// tokens, 32 nodes, 64 / 8 heads: 1.1-1.33 ms (with the clock) for 4.3 GB and 1.1 PFLOP; the copies alone take 0.67 ms, the
-// MMAs alone 0.51 at their rate of 65 clocks, the exponentials of two streams 2320 clocks a key tile;
-// what is left is the chain of one stream's tile, S to P to PV to the next S, 4000 clocks, half of it
-// covered by the other stream.  E4M3, up to 8 nodes: 0.18-0.19 ms for 0.58 GB, bound by the widening of V.
+// What bounds it (cold L2, plan and merge included; figures move with the box's clock).  64 requests of 512-8192
+// tokens, up to 16 nodes, 32 / 8 heads: 218-240 us for 1.15 GB at page size 1, 210 where that takes 218 at page size
+// 16: the copies, in pieces of 256 bytes, one KV head's row of a slot, by 144 of 148 SMs (loads alone 207-222).
+// 8 x 128k tokens, 32 nodes, 64 / 8 heads: 1.14-1.34 ms for 4.3 GB and 1.1 PFLOP.  With all barriers in place the
+// copies alone take 0.67 ms, the MMAs alone 0.82 (0.48 by 65 clocks each at 1965 MHz), the softmax alone 0.75, the
+// barriers without work 0.56; the exponentials of two streams are 2320 clocks a key tile.  What is left is the chain
+// of one stream's tile, S to P to PV to the next S, 4000 clocks, half of it covered by the other stream.  E4M3, up to
+// 8 nodes: 0.19-0.2 ms for 0.58 GB, bound by the widening of V; wide trees are slower than in bf16, since one warp
+// splits Q in front of every query tile (16 requests of 128-256 nodes, G 8, prefixes of 0-500 keys: 362 us, bf16 132).
 // Tried and slower: S in steps of 64 keys with two buffers (an MMA of N 64 takes 49 clocks, of N 128
 // 65); an issuing warp a stream (their MMAs interleave and both streams' scores come at once); four
 // softmax warpgroups of half a key tile each; two regions of 64 score columns a stream, so that the next

@@ -12,7 +12,7 @@
 // Block 0 does the partition (integer, latency-bound: two block-wide scans), the other blocks
 // write the visibility rows, one warp per request; a node's walk up its parents runs in shared
 // memory, so its cost is the node's depth, not a chain of global loads.
-// 64 requests of up to 16 nodes: 4.8 us.
+// 64 requests of up to 16 nodes: 4.2-4.4 us, replayed.
 #include <algorithm>
 
 #include "kernels.h"
@@ -22,7 +22,10 @@ namespace pa {
 namespace {
 
 constexpr int kPlanThreads = 1024;               // for more than kSmallBatch requests
-constexpr int kSmallBatch = 256;                 // up to here 256 threads: barriers of 32 warps cost more than they gain
+// up to here 256 threads: barriers of 32 warps cost more than they gain (65 requests of up to 16 nodes: 4.6 us against
+// 5.0 with 1024).  Towards the border they gain as much and more: 100 requests 5.0 against 5.1, 256 7.4 against 6.2, and
+// with up to 64 nodes, whose rows the fewer threads write, 256 requests 17.0 against 9.5.
+constexpr int kSmallBatch = 256;
 
 // Length, first row and node count of request r; false (n = 0) if they are out of range.
 __device__ bool read_request(const TreePlanLaunch& a, int r, int* L, int* q0, int* n) {

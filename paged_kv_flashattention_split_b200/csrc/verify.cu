@@ -20,8 +20,9 @@
 // cluster barrier later every rank has the sum.  The final token is found by the CTA whose part
 // holds it: from the totals, its chunk sums, then one chunk read again.
 // What bounds it is the chain of passes of the request with the most rejections, each a read of its
-// rows (from L2 after the first).  64 requests, trees of 8-32 nodes over 128k tokens: 50 us, of which the
-// first pass, from HBM, is 10 (rows kept in shared memory between the passes: 56); 16 requests without draft rows, 64 nodes: 14 us; one chain of 8: 11 us.
+// rows (from L2 after the first).  64 requests, trees of 8-32 nodes over 128k tokens: 47-52 us, of which
+// the first pass, from HBM, is 10 (rows kept in shared memory between the passes: 56); 16 requests without draft
+// rows, 64 nodes: 14 us; one chain of 8: 12 us.
 //
 // All weights and sums are 64-bit: a cumulative sum over 10^5 tokens in 32 bits is off by more
 // than the gaps between neighbouring tokens' intervals.  The sums' order is fixed, so results
@@ -399,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyLaunch a) {
 
 cudaError_t launch_tree_verify(const VerifyLaunch& a, cudaStream_t s) {
   // CTAs a request: up to four an SM in all (two are resident: requests end at different times), and
-  // work for half of a CTA's warps.  64 requests over 128k tokens: 51 us with 8 (this rule), 55 with 4,
-  // 78 with 2.
+  // work for half of a CTA's warps.  Trees of 8-32 nodes over 128k tokens with draft rows, up to 2 / 4 / 8 an SM:
+  // 64 requests 57 / 53 / 53 us, 75 88 / 74 / 68, 148 98 / 92 / 102, 200 145 / 102 / 94.  Without draft rows, where
+  // there is one pass and no chain, two an SM would be ahead: 64 requests 23 / 29 / 31, 148 31 / 47 / 59.
   int dev = 0, sms = 148;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
