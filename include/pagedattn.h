@@ -448,7 +448,7 @@ pa_status attn_tree_paged_fp8(const pa_plan_params* params, const void* d_ws, si
  * distributed as samples of the target.  All weights and sums are computed in 64 bits, in a fixed order.
  *
  * d_cu_seqlens_q int32 [B + 1], d_parent int32 [sum n] as for attn_plan_tree (at most 256 nodes
- * a request; sum n <= max_q_tokens); roots other than node 0 are never reached.
+ * a request; cu_seqlens_q[B] <= max_q_tokens); roots other than node 0 are never reached.
  * d_tokens int32 [sum n] (node 0's is not read);  d_target_probs, d_draft_probs fp32 [sum n][vocab],
  * rows target_pitch, draft_pitch >= vocab values apart (draft_pitch 0 without draft rows);
  * vocab <= 2^20.  d_u_accept fp32 [sum n] (node 0's is not read), d_u_final fp32 [B].
@@ -478,7 +478,8 @@ pa_status attn_tree_verify(int32_t batch, int32_t max_q_tokens, int32_t vocab, c
  *                 K and V pools [num_slots][Hkv][D] of elem_bytes (2: bf16, 1: FP8) a value,
  *                 16-byte aligned, that do not overlap (else PA_ERR_INVALID).  Not for Sage pools,
  *                 whose rows belong to their block's scale.
- * d_seq_lens, d_cu_seqlens_q, d_page_table [B][pt_pitch], page_size: as planned;
+ * d_seq_lens, d_cu_seqlens_q, d_page_table [B][pt_pitch], page_size: as planned; max_q_tokens: a
+ * bound on cu_seqlens_q[B], held against the offsets only;
  * d_accept_len, d_accept_path [B][path_pitch]: from attn_tree_verify (path[k] >= k).
  * d_seq_lens_out  int32 [B] or NULL; not the memory of another argument.
  * The positions behind the prefixes must not be shared between requests.
